@@ -64,6 +64,7 @@ extern "C" {
 
 #define RKV_DTYPE_BF16 0
 #define RKV_DTYPE_F32 1
+#define RKV_DTYPE_F16 2           /* prompt attention and the 8-bit block cache only */
 
 #define RKV_MAX_BATCH 256         /* sequences per cache */
 #define RKV_MAX_K 16              /* neighbours per token */
@@ -427,6 +428,203 @@ RKV_API rkv_status rkv_read_device_error(const rkv_cache_desc* desc, void* strea
  * unaligned err_dev.
  */
 RKV_API rkv_status rkv_selftest_wait_timeout(int32_t* err_dev, void* stream);
+
+/* ---- attention over whole prompts -------------------------------------------------------
+ *
+ * Causal attention of a batch of prompts (or of their next chunks) over their own keys and
+ * values: what a layer runs on a prompt before rkv_compress or rkv_kv8_store keeps its K and V
+ * (no counterpart on the pages, which take the prompt's K and V as given).
+ *
+ *   head_dim        64 or 128
+ *   n_kv_heads      key/value heads; n_q_heads a multiple of it, at most 16 times as many
+ *   batch           sequences, 1..RKV_MAX_BATCH
+ *   in_dtype        RKV_DTYPE_BF16 or RKV_DTYPE_F16, for q, K and V
+ *   out_dtype       in_dtype or RKV_DTYPE_F32
+ *   kv_padded       0: the rows of K and V of all sequences lie in one plane of kv_rows rows
+ *                   (packed).  1: sequence b has a plane of kv_rows rows of its own, `kv_plane_stride`
+ *                   apart (the layout that rkv_build_refs and rkv_compress read)
+ *   scale           factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, finite
+ *   q_rows          rows of q, out and lse;  kv_rows  rows of a plane of K and V
+ *   *_stride        element strides: of a row (token), of a head, of a plane.  Those of q, K and V are
+ *                   multiples of 8 and rows of one head are head_dim contiguous elements; out_*
+ *                   multiples of 8 for 16-bit outputs and of 4 for 32-bit ones.
+ *                   K and V share their strides.
+ */
+typedef struct rkv_prefill_config {
+    int32_t head_dim;
+    int32_t n_kv_heads;
+    int32_t n_q_heads;
+    int32_t batch;
+    int32_t in_dtype;
+    int32_t out_dtype;
+    int32_t kv_padded;
+    float scale;
+    int64_t q_rows;
+    int64_t kv_rows;
+    int64_t q_row_stride;
+    int64_t q_head_stride;
+    int64_t kv_row_stride;
+    int64_t kv_head_stride;
+    int64_t kv_plane_stride;
+    int64_t out_row_stride;
+    int64_t out_head_stride;
+} rkv_prefill_config;
+
+/*
+ * For row i (0 <= i < n_b) of sequence b, with n_b = q_off[b+1] - q_off[b] query rows and L_b keys:
+ *   out = sum_j softmax_j(scale * q_i . k_j) v_j   over keys j <= L_b - n_b + i,
+ * so the last query row sees every key: a whole prompt has L_b = n_b; the next chunk of a prompt,
+ * or a single new token, has the keys before it in K and V as well.  A row that sees no key (L_b <
+ * n_b) gives zeros and a log-sum of -inf.  Query head g attends with kv-head g / (n_q_heads / n_kv_heads).
+ *   q_off    device int32 [batch + 1]: sequence b's query rows are q_off[b] .. q_off[b+1] - 1
+ *   kv_off   device int32 [batch + 1] or NULL.  Packed: sequence b's keys are the rows kv_off[b] ..
+ *            kv_off[b+1] - 1 of the plane; NULL means q_off.  Padded: only its first batch entries count,
+ *            sequence b's keys start at row kv_off[b] of its plane; NULL means row 0
+ *   kv_len   device int32 [batch] or NULL: L_b.  NULL means kv_off[b+1] - kv_off[b] (packed), n_b (padded)
+ *   out      [q_rows] rows of n_q_heads x head_dim (strides above); rows outside every sequence keep
+ *            what they held
+ *   lse      NULL or device float [q_rows][n_q_heads]: natural log of sum_j exp(scale * q_i . k_j)
+ *   device_status  device int32, zeroed by the caller before the first use.  A sequence whose rows lie
+ *            outside q or K is skipped and RKV_ERR_INVALID_ARG recorded there (the first error stays); a
+ *            bounded wait that ran out records RKV_ERR_TIMEOUT
+ * Rows of K and V outside a sequence's keys may hold anything (NaN too) and do not reach it, but a
+ * plane's kv_rows rows must be readable.  A non-finite key or value inside a sequence may reach
+ * earlier rows of the same 128 keys too.  q, K, V 16-byte aligned.  q, K, V must not overlap out or lse.
+ * Softmax statistics and sums are 32-bit; the weights enter the second product in in_dtype.  No
+ * workspace; calls on any streams may overlap.
+ */
+RKV_API rkv_status rkv_prefill_attn(const rkv_prefill_config* cfg, const void* q, const void* K, const void* V,
+                                    const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_len, void* out,
+                                    float* lse, int32_t* device_status, void* stream);
+
+/* ---- block tables ------------------------------------------------------------------------
+ *
+ * A block cache keeps the tokens of all requests in blocks of block_size tokens.  Request b's token
+ * p lies in block table[b][p / block_size]; the slot of a token is block * block_size + p % block_size.
+ * Free blocks are a stack on the device: free_list[0 .. n_free - 1], the top last.  These two calls
+ * keep the tables, on the device and without the host knowing a length.
+ *   batch       requests, 1..RKV_MAX_BATCH
+ *   max_blocks  entries of a table row
+ *   block_size  tokens per block: 16, 32, 64 or 128
+ *   n_blocks    blocks of the pool = capacity of free_list; n_blocks * block_size < 2^31
+ */
+typedef struct rkv_blocks_config {
+    int32_t batch;
+    int32_t max_blocks;
+    int32_t block_size;
+    int32_t n_blocks;
+} rkv_blocks_config;
+
+/*
+ * Room for new tokens: request b holds lengths[b] tokens and gets new_counts[b] more (0 is allowed).
+ * Takes the blocks that are missing from the top of the stack, for request 0 first and for each
+ * request in token order, writes them into the table, and writes the slot of every new token.
+ *   lengths, new_counts  device int32 [batch]
+ *   block_table  device int32 [batch][max_blocks]; only entries of new blocks are written
+ *   free_list    device int32 [n_blocks], read;  n_free  device int32
+ *   new_off      device int32 [batch + 1] out: request b's new tokens are new_off[b] .. new_off[b+1] - 1
+ *                of the packed order (q_off of rkv_prefill_attn)
+ *   slot_map     device int32 [max_new] out: their slots; entries from the total on become -1
+ *   lengths_out  device int32 [batch] out: lengths + new_counts (may be lengths itself)
+ *   n_free_out   device int32 out (may be n_free itself)
+ *   device_status  device int32, zeroed by the caller before the first use
+ * If the blocks do not suffice, a row or slot_map is too short (RKV_ERR_WORKSPACE), or a count is negative
+ * or n_free out of range (RKV_ERR_INVALID_ARG), the error is recorded in device_status and nothing is
+ * taken: new_off becomes all 0, slot_map all -1, lengths and n_free stay.  A block id outside the pool
+ * gives slot -1 and RKV_ERR_CORRUPT.  Other than as said, buffers must not overlap.
+ */
+RKV_API rkv_status rkv_blocks_extend(const rkv_blocks_config* cfg, const int32_t* lengths, const int32_t* new_counts,
+                                     int32_t* block_table, const int32_t* free_list, const int32_t* n_free,
+                                     int32_t* new_off, int32_t* slot_map, int64_t max_new, int32_t* lengths_out,
+                                     int32_t* n_free_out, int32_t* device_status, void* stream);
+
+/*
+ * Requests that end: pushes the blocks of every request with ended[b] != 0 (device int32 [batch]) on the
+ * stack, request 0's first and each in token order, and sets its length to 0.  Table rows are left as
+ * they are.  If a length does not fit its row or the stack would overflow (a block given back twice),
+ * RKV_ERR_CORRUPT is recorded and nothing changes; a block id outside the pool is pushed and recorded as
+ * RKV_ERR_CORRUPT.  lengths_out may be lengths, n_free_out may be n_free.
+ */
+RKV_API rkv_status rkv_blocks_release(const rkv_blocks_config* cfg, const int32_t* lengths, const int32_t* ended,
+                                      const int32_t* block_table, int32_t* free_list, const int32_t* n_free,
+                                      int32_t* lengths_out, int32_t* n_free_out, int32_t* device_status, void* stream);
+
+/* ---- 8-bit block cache ---------------------------------------------------------------------
+ *
+ * K and V in 8 bits with one fp32 scale for each block of tokens and kv-head: value = code * scale.
+ * The uncompressed-reference alternative to the residual cache for pooled serving (no counterpart on the
+ * pages).  Buffers are the caller's:
+ *   codes_K, codes_V  [n_blocks][n_kv_heads][block_size][head_dim] bytes, 16-byte aligned
+ *   scale_K, scale_V  [n_blocks][n_kv_heads] float
+ *   device_status     device int32, zeroed by the caller before the first use
+ *   code_type    RKV_KV8_INT8: codes -127..127; RKV_KV8_E4M3: 8-bit floats, 4 exponent and 3 mantissa
+ *                bits, largest 448.  qmax is 127 or 448
+ *   in_dtype     RKV_DTYPE_BF16 or RKV_DTYPE_F16: K, V and q;  out_dtype  in_dtype or RKV_DTYPE_F32
+ *   n_q_heads    a multiple of n_kv_heads, at most 16 times as many
+ *   batch, max_blocks, block_size, n_blocks  as rkv_blocks_config
+ *   scale        factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, finite
+ */
+#define RKV_KV8_INT8 0
+#define RKV_KV8_E4M3 1
+typedef struct rkv_kv8_cache {
+    int32_t head_dim;
+    int32_t n_kv_heads;
+    int32_t n_q_heads;
+    int32_t block_size;
+    int32_t n_blocks;
+    int32_t max_blocks;
+    int32_t batch;
+    int32_t code_type;
+    int32_t in_dtype;
+    int32_t out_dtype;
+    float scale;
+    int32_t reserved;
+    uint8_t* codes_K;
+    uint8_t* codes_V;
+    float* scale_K;
+    float* scale_V;
+    int32_t* device_status;
+} rkv_kv8_cache;
+
+/*
+ * Writes n_rows new rows of K and V into the cache.
+ *   K_new, V_new  row r of kv-head h at r * row_stride + h * head_stride elements (multiples of 8), head_dim
+ *                 contiguous elements, 16-byte aligned
+ *   slot_map      device int32 [n_rows]: row r's slot; a negative slot skips its row
+ * The rows that one call puts into a block are consecutive rows with ascending consecutive slots, and a
+ * block is filled from slot 0 of it upwards (rkv_blocks_extend's slots are so); two runs of rows into the
+ * same block in one call leave its contents unspecified.  For each such run, with a the largest |x| of its
+ * rows and need = max(fl32(a * fl32(1 / qmax)), 2^-64) (0 if a is 0):
+ *   - a run that starts a block sets scale = need;
+ *   - a run that goes on in a block keeps its scale if scale >= need, else takes scale * 2^m with the smallest
+ *     m that reaches need, and the codes already in the block become round(code * 2^-m) (each such step
+ *     at least doubles the scale, so their total rounding error stays under one step of the last scale);
+ *     a scale of 0 becomes need;
+ *   - code = round(fl32(x / scale)), half to even, 0 where the scale is 0.
+ * A NaN is stored as 0 and an infinity as the largest code with its sign, and RKV_ERR_INVALID_ARG is
+ * recorded in device_status; neither counts in a.  A slot outside the pool skips its row and records
+ * RKV_ERR_CORRUPT.  Calls that write one cache run in order (one stream, or events).
+ */
+RKV_API rkv_status rkv_kv8_store(const rkv_kv8_cache* cache, const void* K_new, const void* V_new, int64_t row_stride,
+                                 int64_t head_stride, const int32_t* slot_map, int64_t n_rows, void* stream);
+
+/* Bytes of rkv_kv8_decode_attn's workspace for this cache (host only). */
+RKV_API rkv_status rkv_kv8_workspace(const rkv_kv8_cache* cache, uint64_t* bytes);
+
+/*
+ * Attention of one new token per request over its cached tokens: for every query head g of request b
+ *   out[b][g] = sum_i softmax_i(scale * q[b][g] . K_i) V_i   over the request's lengths[b] tokens.
+ *   q            [batch][n_q_heads][head_dim] in_dtype, out the same shape in out_dtype; 16-byte aligned
+ *   block_table  device int32 [batch][max_blocks];  lengths  device int32 [batch]: tokens to attend to (the new
+ *                token's own row is stored before); 0 gives zeros
+ *   workspace    device, 256-byte aligned, >= rkv_kv8_workspace's size; scratch of one call, needs no
+ *                initialisation; calls that overlap need different workspaces
+ * A length that its table row cannot hold is clamped to it, and blocks outside the pool are skipped; both record
+ * RKV_ERR_CORRUPT in device_status.  Results do not depend on timing (no atomics).
+ */
+RKV_API rkv_status rkv_kv8_decode_attn(const rkv_kv8_cache* cache, const void* q, const int32_t* block_table,
+                                       const int32_t* lengths, void* out, void* workspace, uint64_t workspace_bytes,
+                                       void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,6 +18,9 @@ LIB_PATH = os.path.join(_HERE, "librkv.so")
 
 RKV_DTYPE_BF16 = 0
 RKV_DTYPE_F32 = 1
+RKV_DTYPE_F16 = 2
+RKV_KV8_INT8 = 0
+RKV_KV8_E4M3 = 1
 RKV_FLAG_SELECT_SIMT = 0x1
 RKV_FLAG_DECODE_DIRECT = 0x2
 RKV_FLAG_DECODE_SIMT = 0x4
@@ -31,7 +34,8 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 EXPORTED = ["rkv_abi_version", "rkv_status_string", "rkv_schedule", "rkv_cache_size", "rkv_cache_bind",
             "rkv_unit_view_get", "rkv_build_refs", "rkv_search", "rkv_encode", "rkv_compress", "rkv_decode_attn", "rkv_reconstruct",
             "rkv_read_device_error", "rkv_compress_noalloc", "rkv_decode_attn_sparse", "rkv_cache_set_lengths",
-            "rkv_append", "rkv_set_coder", "rkv_selftest_wait_timeout"]
+            "rkv_append", "rkv_set_coder", "rkv_selftest_wait_timeout", "rkv_prefill_attn", "rkv_blocks_extend",
+            "rkv_blocks_release", "rkv_kv8_store", "rkv_kv8_workspace", "rkv_kv8_decode_attn"]
 
 
 class RkvError(RuntimeError):
@@ -52,6 +56,25 @@ class rkv_unit_view(ctypes.Structure):
                                               "reserved")] + \
                [(n, ctypes.c_void_p) for n in ("ref_K", "ref_V", "ref_half_norm", "ref_pos", "codes_K", "codes_V",
                                                "scale_K", "scale_V", "idx", "ref_scale_K", "ref_scale_V")]
+
+
+class rkv_prefill_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "n_kv_heads", "n_q_heads", "batch", "in_dtype", "out_dtype",
+                                              "kv_padded")] + [("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("q_rows", "kv_rows", "q_row_stride", "q_head_stride", "kv_row_stride",
+                                              "kv_head_stride", "kv_plane_stride", "out_row_stride",
+                                              "out_head_stride")]
+
+
+class rkv_blocks_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "max_blocks", "block_size", "n_blocks")]
+
+
+class rkv_kv8_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "n_kv_heads", "n_q_heads", "block_size", "n_blocks",
+                                              "max_blocks", "batch", "code_type", "in_dtype", "out_dtype")] + \
+               [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("codes_K", "codes_V", "scale_K", "scale_V", "device_status")]
 
 
 _lib = None
@@ -86,6 +109,12 @@ def lib() -> ctypes.CDLL:
         L.rkv_append.argtypes = [vp, vp, vp, vp, vp]
         L.rkv_set_coder.argtypes = [vp, vp]
         L.rkv_selftest_wait_timeout.argtypes = [vp, vp]
+        L.rkv_prefill_attn.argtypes = [vp] * 11
+        L.rkv_blocks_extend.argtypes = [vp] * 8 + [i64] + [vp] * 4
+        L.rkv_blocks_release.argtypes = [vp] * 10
+        L.rkv_kv8_store.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp]
+        L.rkv_kv8_workspace.argtypes = [vp, ctypes.POINTER(u64)]
+        L.rkv_kv8_decode_attn.argtypes = [vp] * 6 + [u64, vp]
         for name in EXPORTED[2:]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -137,6 +166,32 @@ def make_config(head_dim, n_kv_heads, n_q_heads, k, bits, stride0, batch, max_le
     1 the learned-coder shapes (weights bound with rkv_set_coder)."""
     return rkv_config(head_dim, n_kv_heads, n_q_heads, k, bits, group, stride0, refs_per_phase, in_dtype,
                       in_dtype if out_dtype is None else out_dtype, batch, max_len, flags, ref_bits, coder, 0)
+
+
+def make_prefill_config(head_dim, n_kv_heads, n_q_heads, batch, q_rows, kv_rows, in_dtype=RKV_DTYPE_BF16,
+                        out_dtype=None, kv_padded=False, scale=0.0, q_strides=None, kv_strides=None,
+                        out_strides=None) -> rkv_prefill_config:
+    """Strides in elements, contiguous layouts by default: q and out [q_rows][n_q_heads][head_dim] (row, head);
+    K and V packed [kv_rows][n_kv_heads][head_dim] or, with kv_padded, [batch][n_kv_heads][kv_rows][head_dim],
+    the layout of rkv_compress (row, head, plane)."""
+    D = head_dim
+    qs = (n_q_heads * D, D) if q_strides is None else q_strides
+    os_ = (n_q_heads * D, D) if out_strides is None else out_strides
+    if kv_strides is None:
+        kv_strides = (D, max(1, kv_rows) * D, n_kv_heads * max(1, kv_rows) * D) if kv_padded else (n_kv_heads * D, D, 0)
+    return rkv_prefill_config(D, n_kv_heads, n_q_heads, batch, in_dtype, in_dtype if out_dtype is None else out_dtype,
+                              1 if kv_padded else 0, scale, q_rows, kv_rows, qs[0], qs[1], *kv_strides, *os_)
+
+
+def make_blocks_config(batch, max_blocks, block_size, n_blocks) -> rkv_blocks_config:
+    return rkv_blocks_config(batch, max_blocks, block_size, n_blocks)
+
+
+def make_kv8_config(head_dim, n_kv_heads, n_q_heads, block_size, n_blocks, max_blocks, batch, code_type=RKV_KV8_INT8,
+                    in_dtype=RKV_DTYPE_BF16, out_dtype=None, scale=0.0) -> rkv_kv8_cache:
+    """Shape of an 8-bit block cache; KV8Cache fills in the buffers."""
+    return rkv_kv8_cache(head_dim, n_kv_heads, n_q_heads, block_size, n_blocks, max_blocks, batch, code_type, in_dtype,
+                         in_dtype if out_dtype is None else out_dtype, scale, 0)
 
 
 # --- the C ABI, one function each ------------------------------------------------------
@@ -247,6 +302,62 @@ def rkv_selftest_wait_timeout(err_dev, stream=None):
     _check(lib().rkv_selftest_wait_timeout(_ptr(err_dev), _stream(stream)), "rkv_selftest_wait_timeout")
 
 
+def _same_device(where: str, *tensors):
+    """Tensors of another device than the current one (whose stream the call uses) are refused."""
+    import torch
+
+    cur = torch.cuda.current_device()
+    for x in tensors:
+        if x is not None and hasattr(x, "get_device") and x.get_device() != cur:
+            raise RkvError(STATUS_CODE["RKV_ERR_INVALID_ARG"], f"{where}: a tensor on {x.device}, not on cuda:{cur}")
+
+
+def rkv_prefill_attn(cfg: rkv_prefill_config, q, K, V, q_off, kv_off, kv_len, out, lse, device_status, stream=None):
+    _same_device("rkv_prefill_attn", q, K, V, q_off, kv_off, kv_len, out, lse, device_status)
+    _check(lib().rkv_prefill_attn(ctypes.addressof(cfg), _ptr(q), _ptr(K), _ptr(V), _ptr(q_off), _ptr(kv_off),
+                                  _ptr(kv_len), _ptr(out), _ptr(lse), _ptr(device_status), _stream(stream)),
+           "rkv_prefill_attn")
+
+
+def rkv_blocks_extend(cfg: rkv_blocks_config, lengths, new_counts, block_table, free_list, n_free, new_off, slot_map,
+                      max_new: int, lengths_out, n_free_out, device_status, stream=None):
+    _same_device("rkv_blocks_extend", lengths, new_counts, block_table, free_list, n_free, new_off, slot_map,
+                 lengths_out, n_free_out, device_status)
+    _check(lib().rkv_blocks_extend(ctypes.addressof(cfg), _ptr(lengths), _ptr(new_counts), _ptr(block_table),
+                                   _ptr(free_list), _ptr(n_free), _ptr(new_off), _ptr(slot_map), max_new,
+                                   _ptr(lengths_out), _ptr(n_free_out), _ptr(device_status), _stream(stream)),
+           "rkv_blocks_extend")
+
+
+def rkv_blocks_release(cfg: rkv_blocks_config, lengths, ended, block_table, free_list, n_free, lengths_out, n_free_out,
+                       device_status, stream=None):
+    _same_device("rkv_blocks_release", lengths, ended, block_table, free_list, n_free, lengths_out, n_free_out,
+                 device_status)
+    _check(lib().rkv_blocks_release(ctypes.addressof(cfg), _ptr(lengths), _ptr(ended), _ptr(block_table),
+                                    _ptr(free_list), _ptr(n_free), _ptr(lengths_out), _ptr(n_free_out),
+                                    _ptr(device_status), _stream(stream)), "rkv_blocks_release")
+
+
+def rkv_kv8_store(cache: rkv_kv8_cache, K_new, V_new, row_stride: int, head_stride: int, slot_map, n_rows: int,
+                  stream=None):
+    _same_device("rkv_kv8_store", K_new, V_new, slot_map)
+    _check(lib().rkv_kv8_store(ctypes.addressof(cache), _ptr(K_new), _ptr(V_new), row_stride, head_stride,
+                               _ptr(slot_map), n_rows, _stream(stream)), "rkv_kv8_store")
+
+
+def rkv_kv8_workspace(cache: rkv_kv8_cache) -> int:
+    n = ctypes.c_uint64(0)
+    _check(lib().rkv_kv8_workspace(ctypes.addressof(cache), ctypes.byref(n)), "rkv_kv8_workspace")
+    return n.value
+
+
+def rkv_kv8_decode_attn(cache: rkv_kv8_cache, q, block_table, lengths, out, workspace, workspace_bytes: int,
+                        stream=None):
+    _same_device("rkv_kv8_decode_attn", q, block_table, lengths, out, workspace)
+    _check(lib().rkv_kv8_decode_attn(ctypes.addressof(cache), _ptr(q), _ptr(block_table), _ptr(lengths), _ptr(out),
+                                     _ptr(workspace), workspace_bytes, _stream(stream)), "rkv_kv8_decode_attn")
+
+
 # --- buffers ---------------------------------------------------------------------------
 
 class Layer:
@@ -307,3 +418,111 @@ class Layer:
 
     def unit(self, seq: int, kv_head: int) -> rkv_unit_view:
         return rkv_unit_view_get(self.desc, seq, kv_head)
+
+
+def _refuse(where: str, why: str):
+    raise RkvError(STATUS_CODE["RKV_ERR_INVALID_ARG"], f"{where} ({why})")
+
+
+def _take_error(status) -> int:
+    """Reads and clears a device status word (waits for the current stream)."""
+    v = int(status.item())
+    if v:
+        status.zero_()
+    return v
+
+
+class Prefill:
+    """Causal attention over packed prompts: a configuration and its device status word."""
+
+    def __init__(self, cfg: rkv_prefill_config, device="cuda"):
+        import torch
+
+        self.cfg = cfg
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def attend(self, q, K, V, q_off, out, kv_off=None, kv_len=None, lse=None, stream=None):
+        """q_off, kv_off: int32 [batch + 1], kv_len: int32 [batch], all on the device; layouts as in
+        make_prefill_config."""
+        rkv_prefill_attn(self.cfg, q, K, V, q_off, kv_off, kv_len, out, lse, self.status, stream)
+
+    def device_error(self) -> int:
+        return _take_error(self.status)
+
+
+class BlockTables:
+    """Block table, free stack and lengths of the requests of a block cache, kept on the device."""
+
+    def __init__(self, batch, max_blocks, block_size, n_blocks, device="cuda"):
+        import torch
+
+        self.cfg = make_blocks_config(batch, max_blocks, block_size, n_blocks)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.table = torch.full((batch, max_blocks), -1, **i32)
+        self.free_list = torch.arange(n_blocks - 1, -1, -1, **i32)     # block 0 on top
+        self.n_free = torch.full((1,), n_blocks, **i32)
+        self.lengths = torch.zeros(batch, **i32)
+        self.new_off = torch.zeros(batch + 1, **i32)
+        self.status = torch.zeros(1, **i32)
+
+    def extend(self, new_counts, slot_map, stream=None):
+        """Room for new_counts[b] more tokens of each request; their slots go to slot_map (int32, -1 behind the
+        last), their packed offsets to new_off, and lengths grows."""
+        rkv_blocks_extend(self.cfg, self.lengths, new_counts, self.table, self.free_list, self.n_free, self.new_off,
+                          slot_map, slot_map.numel(), self.lengths, self.n_free, self.status, stream)
+
+    def release(self, ended, stream=None):
+        """The blocks of the requests with a nonzero flag go back, their lengths become 0."""
+        rkv_blocks_release(self.cfg, self.lengths, ended, self.table, self.free_list, self.n_free, self.lengths,
+                           self.n_free, self.status, stream)
+
+    def device_error(self) -> int:
+        return _take_error(self.status)
+
+
+class KV8Cache:
+    """One layer's 8-bit block cache: codes [n_blocks, kv_heads, block_size, head_dim] (int8 or float8_e4m3fn) and
+    scales [n_blocks, kv_heads] (float32), allocated here unless given, and the decode's workspace."""
+
+    def __init__(self, cfg: rkv_kv8_cache, codes_K=None, codes_V=None, scale_K=None, scale_V=None, device="cuda",
+                 workspace=None):
+        import torch
+
+        self.ws_bytes = rkv_kv8_workspace(cfg)                         # refuses an impossible shape
+        shape = (cfg.n_blocks, cfg.n_kv_heads, cfg.block_size, cfg.head_dim)
+        kind = torch.int8 if cfg.code_type == RKV_KV8_INT8 else torch.float8_e4m3fn
+
+        def buffer(x, shape, dtype, name):
+            if x is None:
+                return torch.zeros(shape, dtype=torch.uint8 if dtype is kind else dtype, device=device).view(dtype)
+            if tuple(x.shape) != shape or x.dtype is not dtype or not x.is_contiguous():
+                _refuse("KV8Cache", f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+            return x
+
+        self.codes_K = buffer(codes_K, shape, kind, "codes_K")
+        self.codes_V = buffer(codes_V, shape, kind, "codes_V")
+        self.scale_K = buffer(scale_K, shape[:2], torch.float32, "scale_K")
+        self.scale_V = buffer(scale_V, shape[:2], torch.float32, "scale_V")
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        if workspace is None:
+            workspace = torch.empty(max(256, self.ws_bytes), dtype=torch.uint8, device=device)
+        self.workspace = workspace
+        _same_device("KV8Cache", self.codes_K, self.codes_V, self.scale_K, self.scale_V, self.workspace)
+        self.c = rkv_kv8_cache.from_buffer_copy(cfg)
+        for name in ("codes_K", "codes_V", "scale_K", "scale_V"):
+            setattr(self.c, name, getattr(self, name).data_ptr())
+        self.c.device_status = self.status.data_ptr()
+
+    def store(self, K_new, V_new, slot_map, stream=None):
+        """K_new, V_new: [rows, kv_heads, head_dim] with the same row and head strides and contiguous channels;
+        slot_map: int32 [rows] (negative: the row is skipped)."""
+        if K_new.stride() != V_new.stride() or K_new.stride(2) != 1:
+            _refuse("KV8Cache.store", "K_new and V_new must have equal strides and contiguous channels")
+        rkv_kv8_store(self.c, K_new, V_new, K_new.stride(0), K_new.stride(1), slot_map, K_new.shape[0], stream)
+
+    def decode(self, q, block_table, lengths, out, stream=None):
+        """q, out: [batch, q_heads, head_dim]; block_table: int32 [batch, max_blocks]; lengths: int32 [batch]."""
+        rkv_kv8_decode_attn(self.c, q, block_table, lengths, out, self.workspace, self.workspace.numel(), stream)
+
+    def device_error(self) -> int:
+        return _take_error(self.status)

@@ -2,38 +2,24 @@
 // Every entry point returns an rkv_status and never throws; see include/rkv.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <atomic>
 #include <climits>
-#include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <new>
 #include <vector>
 
+#include "api_common.h"
 #include "launchers.h"
 #include "rkv.h"
 #include "rkv_internal.h"
 
 using namespace rkv;
+using namespace rkv::api;
 
 namespace {
-
-// An NVTX range around one entry point, so a profile of the whole path splits by API call.
-// Costs a few nanoseconds when no profiler is attached.
-struct ApiRange {
-    explicit ApiRange(const char* name) { nvtxRangePushA(name); }
-    ~ApiRange() { nvtxRangePop(); }
-    ApiRange(const ApiRange&) = delete;
-    ApiRange& operator=(const ApiRange&) = delete;
-};
-
-uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---- reference schedule on the host ----------------------------------------------------
 
@@ -279,20 +265,6 @@ CacheArgs make_args(const Desc& d)
     a.idx = reinterpret_cast<uint16_t*>(base + d.sec.idx);
     return a;
 }
-
-// A failed CUDA call becomes RKV_ERR_CUDA; with RKV_DEBUG set in the environment its
-// CUDA error string is also printed to stderr.
-rkv_status cuda_status(cudaError_t e)
-{
-    if (e == cudaSuccess)
-        return RKV_OK;
-    static const bool verbose = std::getenv("RKV_DEBUG") != nullptr;
-    if (verbose)
-        std::fprintf(stderr, "librkv: CUDA error %d: %s\n", static_cast<int>(e), cudaGetErrorString(e));
-    return RKV_ERR_CUDA;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
 

@@ -1,0 +1,280 @@
+// Block tables and slot maps of a block cache, kept on the device.
+//
+// With have_b = ceil(len_b / s) and need_b = ceil((len_b + new_b) / s) blocks of s tokens, request
+// b's missing blocks m_b = need_b - have_b come off the top of the free stack in request order:
+//   table[b][have_b + i] = free[n_free - 1 - (M_b + i)],  M_b = sum_{c < b} m_c, i < m_b
+// and new token t of the packed order (request b, position p = len_b + t - N_b, N_b = sum_{c < b}
+// new_c) gets slot table[b][p / s] * s + p % s.  Giving back is the reverse: the blocks of the ended
+// requests go on the stack in request order.
+//
+// One launch each.  Every CTA reads all lengths (at most 256) and forms both prefix sums itself, in
+// shared memory, so nothing has to be handed over between kernels; the CTAs then share the output
+// entries.  They form one cluster, whose barrier separates the last read of the lengths and of the
+// stack's height from the first write, so both may be updated in place.  A token finds its request
+// by a binary search of the prefix sums (8 steps in shared memory).
+#include <cooperative_groups.h>
+
+#include "device_common.cuh"
+#include "launchers.h"
+
+namespace rkv {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512;
+static_assert(kThreads >= RKV_MAX_BATCH, "one thread per request in the prefix sums");
+
+// Inclusive sums over the first RKV_MAX_BATCH threads of the CTA (the others pass 0 and take part).
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_tot)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t n = __shfl_up_sync(0xffffffffu, v, o);
+        v += (lane >= o) ? n : 0;
+    }
+    __syncthreads();   // the previous scan's totals have been read
+    if (lane == 31)
+        warp_tot[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w)
+        v += warp_tot[w];
+    return v;
+}
+
+// The request whose range [off[b], off[b + 1]) holds x (empty ranges are passed over).
+__device__ __forceinline__ int owner(const int* off, int batch, int x)
+{
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (off[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+constexpr int kNone = INT32_MAX;
+
+struct BlockShared {
+    int64_t warp_tot[kThreads / 32];
+    int off[RKV_MAX_BATCH + 1];    // packed new tokens before request b
+    int more[RKV_MAX_BATCH + 1];   // blocks taken (given back) before request b
+    int have[RKV_MAX_BATCH];       // blocks that the request holds
+    int len[RKV_MAX_BATCH];
+    int bad;                       // smallest status that forbids the call (kNone: none)
+};
+
+__global__ void __launch_bounds__(kThreads)
+    blocks_extend_kernel(const rkv_blocks_config c, int shift, const int32_t* lengths, const int32_t* new_counts,
+                         int32_t* table, const int32_t* __restrict__ free_list, const int32_t* n_free,
+                         int32_t* new_off, int32_t* slot_map, int64_t max_new, int32_t* lengths_out,
+                         int32_t* n_free_out, int32_t* err)
+{
+    __shared__ BlockShared s;
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        s.bad = kNone;
+    __syncthreads();
+    const int nfree = *n_free;
+    int64_t len = 0, add = 0, have = 0, more = 0;
+    if (tid < c.batch) {
+        len = lengths[tid];
+        add = new_counts[tid];
+        const int64_t m = (1 << shift) - 1;
+        const int64_t need = (len + add + m) >> shift;
+        have = (len + m) >> shift;
+        if (len < 0 || add < 0) {
+            atomicMin(&s.bad, RKV_ERR_INVALID_ARG);
+            len = add = have = 0;
+        } else if (need > c.max_blocks) {
+            atomicMin(&s.bad, RKV_ERR_WORKSPACE);
+            add = 0;
+        } else {
+            more = need - have;
+        }
+    }
+    const int64_t tok = block_scan(add, s.warp_tot);
+    const int64_t blk = block_scan(more, s.warp_tot);
+    if (tid < c.batch) {
+        // sums past 31 bits end in `bad` below and are not used
+        s.off[tid + 1] = static_cast<int>(tok < INT32_MAX ? tok : INT32_MAX);
+        s.more[tid + 1] = static_cast<int>(blk < INT32_MAX ? blk : INT32_MAX);
+        s.have[tid] = static_cast<int>(have);
+        s.len[tid] = static_cast<int>(len);
+    }
+    if (tid == 0) {
+        s.off[0] = 0;
+        s.more[0] = 0;
+        if (nfree < 0 || nfree > c.n_blocks)
+            atomicMin(&s.bad, RKV_ERR_INVALID_ARG);
+    }
+    if (tid == c.batch - 1 && (tok > max_new || blk > nfree))
+        atomicMin(&s.bad, RKV_ERR_WORKSPACE);
+    // every CTA has read lengths and n_free: from here on they may be overwritten
+    cg::this_cluster().sync();
+
+    const int gtid = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
+    if (s.bad != kNone) {
+        for (int64_t t = gtid; t < max_new; t += gsize)
+            slot_map[t] = -1;
+        if (blockIdx.x == 0) {
+            if (tid < c.batch) {
+                new_off[tid + 1] = 0;
+                lengths_out[tid] = lengths[tid];
+            }
+            if (tid == 0) {
+                new_off[0] = 0;
+                *n_free_out = nfree;
+                report(err, s.bad);
+            }
+        }
+        return;
+    }
+    const int total = s.off[c.batch], taken = s.more[c.batch];
+    if (blockIdx.x == 0) {
+        if (tid < c.batch) {
+            new_off[tid + 1] = s.off[tid + 1];
+            lengths_out[tid] = static_cast<int>(len + add);
+        }
+        if (tid == 0) {
+            new_off[0] = 0;
+            *n_free_out = nfree - taken;
+        }
+    }
+    bool corrupt = false;
+    for (int i = gtid; i < taken; i += gsize) {
+        const int b = owner(s.more, c.batch, i);
+        table[static_cast<int64_t>(b) * c.max_blocks + s.have[b] + i - s.more[b]] = free_list[nfree - 1 - i];
+    }
+    for (int64_t t = gtid; t < max_new; t += gsize) {
+        int slot = -1;
+        if (t < total) {
+            const int b = owner(s.off, c.batch, static_cast<int>(t));
+            const int p = s.len[b] + static_cast<int>(t) - s.off[b];
+            const int ord = p >> shift;
+            // a block taken by this call is read from the stack (its table entry is being written)
+            const int id = ord < s.have[b] ? table[static_cast<int64_t>(b) * c.max_blocks + ord]
+                                           : free_list[nfree - 1 - (s.more[b] + ord - s.have[b])];
+            if (id >= 0 && id < c.n_blocks)
+                slot = (id << shift) + (p & ((1 << shift) - 1));
+            else
+                corrupt = true;
+        }
+        slot_map[t] = slot;
+    }
+    if (corrupt)
+        report(err, RKV_ERR_CORRUPT);
+}
+
+__global__ void __launch_bounds__(kThreads)
+    blocks_release_kernel(const rkv_blocks_config c, int shift, const int32_t* lengths, const int32_t* ended,
+                          const int32_t* __restrict__ table, int32_t* free_list, const int32_t* n_free,
+                          int32_t* lengths_out, int32_t* n_free_out, int32_t* err)
+{
+    __shared__ BlockShared s;
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        s.bad = kNone;
+    __syncthreads();
+    const int nfree = *n_free;
+    int64_t len = 0, give = 0;
+    bool end = false;
+    if (tid < c.batch) {
+        len = lengths[tid];
+        end = ended[tid] != 0;
+        const int64_t have = (len + (1 << shift) - 1) >> shift;
+        if (len < 0 || have > c.max_blocks)
+            atomicMin(&s.bad, RKV_ERR_CORRUPT);
+        else
+            give = end ? have : 0;
+    }
+    const int64_t sum = block_scan(give, s.warp_tot);
+    if (tid < c.batch)
+        s.more[tid + 1] = static_cast<int>(sum < INT32_MAX ? sum : INT32_MAX);
+    if (tid == 0) {
+        s.more[0] = 0;
+        if (nfree < 0)
+            atomicMin(&s.bad, RKV_ERR_CORRUPT);
+    }
+    if (tid == c.batch - 1 && nfree + sum > c.n_blocks)
+        atomicMin(&s.bad, RKV_ERR_CORRUPT);
+    cg::this_cluster().sync();   // lengths and n_free have been read by every CTA
+
+    const int total = s.bad != kNone ? 0 : s.more[c.batch];
+    if (blockIdx.x == 0) {
+        if (tid < c.batch)
+            lengths_out[tid] = (end && s.bad == kNone) ? 0 : static_cast<int>(len);
+        if (tid == 0) {
+            *n_free_out = nfree + total;
+            if (s.bad != kNone)
+                report(err, s.bad);
+        }
+    }
+    bool corrupt = false;
+    for (int i = blockIdx.x * kThreads + tid; i < total; i += gridDim.x * kThreads) {
+        const int b = owner(s.more, c.batch, i);
+        const int id = table[static_cast<int64_t>(b) * c.max_blocks + i - s.more[b]];
+        corrupt |= id < 0 || id >= c.n_blocks;
+        free_list[nfree + i] = id;
+    }
+    if (corrupt)
+        report(err, RKV_ERR_CORRUPT);
+}
+
+int log2_of(int n)
+{
+    int s = 0;
+    while ((1 << s) < n)
+        ++s;
+    return s;
+}
+
+// CTAs (one cluster) for `work` output entries: one CTA covers a decode step (a few hundred
+// entries) in one pass; eight, the largest portable cluster, share a prompt's tens of thousands.
+int cluster_for(int64_t work) { return work <= 4 * kThreads ? 1 : 8; }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), int ctas, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_blocks_extend(const rkv_blocks_config& c, const int32_t* lengths, const int32_t* new_counts,
+                                 int32_t* table, const int32_t* free_list, const int32_t* n_free, int32_t* new_off,
+                                 int32_t* slot_map, int64_t max_new, int32_t* lengths_out, int32_t* n_free_out,
+                                 int32_t* err, cudaStream_t st)
+{
+    return launch_cluster(blocks_extend_kernel, cluster_for(max_new), st, c, log2_of(c.block_size), lengths,
+                          new_counts, table, free_list, n_free, new_off, slot_map, max_new, lengths_out, n_free_out,
+                          err);
+}
+
+cudaError_t launch_blocks_release(const rkv_blocks_config& c, const int32_t* lengths, const int32_t* ended,
+                                  const int32_t* table, int32_t* free_list, const int32_t* n_free,
+                                  int32_t* lengths_out, int32_t* n_free_out, int32_t* err, cudaStream_t st)
+{
+    // the blocks given back are known on the device only: sized by what the tables could hold
+    const int64_t most = static_cast<int64_t>(c.batch) * c.max_blocks;
+    return launch_cluster(blocks_release_kernel, cluster_for(most), st, c, log2_of(c.block_size), lengths, ended,
+                          table, free_list, n_free, lengths_out, n_free_out, err);
+}
+
+}  // namespace rkv

@@ -1,0 +1,606 @@
+// Attention of one new token per request over the 8-bit block cache.
+//
+//   out_g = sum_i p_i V_i / sum_i p_i,  p_i = exp(scale q_g . K_i),  K_i = sK_blk codeK_i, V_i = sV_blk codeV_i
+//
+// The scales stay out of the products: with x_i = scale log2(e) sK_blk (q_g . codeK_i) the kernel keeps,
+// over the tokens seen so far, M = max_i (x_i + log2 sV_blk) and
+//   O = sum_i w_i codeV_i,  L = sum_i w_i / sV_blk,  w_i = 2^15 2^(x_i + log2 sV_blk - M) <= 2^15,
+// so out = O / L.  Folding the V scale into the exponent bounds every w_i whatever the blocks' scales, so
+// it can enter the second product as a binary16 number (11 significant bits, rounded to nearest: the same
+// or finer than a 16-bit output); the factor 2^15 keeps the weights of a flat context of millions of tokens
+// out of binary16's subnormals.
+//
+// Both products run on warp-level tensor-core instructions (m16n8k16, binary16 in, fp32 out): with at most
+// 8 query heads per kv-head they have a single narrow column tile, 2 x 128 x 8 multiply-adds per 256 bytes, so
+// the kernel is bound by HBM and what counts is that codes go from memory to operand registers without a
+// detour.  They do: the order of the channels inside a product is free, so each lane loads 16 consecutive
+// bytes of a row and uses them as its operand elements (no shared memory, no shuffles):
+//   S^T = K q^T   A = K, 16 tokens x 16 channels.  Lane (g, t) = (lane / 4, lane % 4) holds tokens g and g + 8;
+//                 step s takes its channels 16 t + 4 s .. + 3 (s < 4; + 64 for s >= 4).
+//   O^T = V^T w   A = V^T, 16 channels x 16 tokens.  Lane (g, t) holds tokens 2t, 2t+1, 2t+8, 2t+9, channels
+//                 16 g .. 16 g + 15; row tile i takes channels 16 g + 2 i (rows 0-7) and 16 g + 2 i + 1 (8-15).
+//                 w goes from S^T's accumulator layout to the B operand by one 8x8 transpose per 8 tokens.
+// (With head_dim 64 a lane's piece is 8 bytes of V, and the K steps stop at 4.)
+// int8 codes become binary16 exactly by bytes: 0x6400 | (c + 128) is 1152 + c, minus 1152.  8-bit floats
+// have a conversion instruction; binary16 holds them exactly.  q is scaled by a power of two per head so that
+// its largest element lies in [2^14, 2^15): every element is then exact or, if tiny, off by at most 2^-40 of
+// the largest.
+//
+// Work split: units (request, kv-head) are cut into tiles of 64 tokens; the CTAs take equal contiguous
+// ranges of all tiles, found from the lengths on the device.  A CTA's four warps take 16 tokens of each
+// tile; at the end of a unit its warps' states are merged and either written out (the CTA had the whole
+// unit) or left in the workspace for the join kernel, which adds the parts in order.
+#include <cuda_fp8.h>
+
+#include <cfloat>
+#include <cmath>
+
+#include "kv8_common.cuh"
+#include "launchers.h"
+
+namespace rkv {
+
+namespace {
+
+using namespace kv8;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 16 * kWarps;     // tokens per CTA step
+constexpr int kCtasPerSm = 4;
+constexpr float kNone = -1e30f;        // running maximum before any token
+constexpr float kWeightExp = 15.0f;    // weights are kept times 2^15: binary16 then holds 2^-39 .. 1 of the largest
+
+struct DecodeArgs {
+    int32_t Hkv, Hq, G, batch, block_shift, n_blocks, max_blocks, out_dtype;
+    float qk;                          // scale * log2(e)
+    const uint16_t* q;
+    const uint8_t* codes_K;
+    const uint8_t* codes_V;
+    const float* scale_K;
+    const float* scale_V;
+    const int32_t* table;
+    const int32_t* lengths;
+    void* out;
+    float* parts;                      // [2 * CTAs][heads][D + 2]
+    int32_t* err;
+};
+
+// Tokens of request b that are attended to (its length, clamped to what the table row can hold).
+__device__ __forceinline__ int request_len(const DecodeArgs& a, int b)
+{
+    const int64_t cap = static_cast<int64_t>(a.max_blocks) << a.block_shift;
+    return static_cast<int>(min(static_cast<int64_t>(max(a.lengths[b], 0)), cap));
+}
+
+// Tiles before each request (all its kv-heads), for the whole CTA: pre[b], b = 0 .. batch.
+__device__ __forceinline__ void tile_prefix(const DecodeArgs& a, int64_t* pre)
+{
+    constexpr int kPer = RKV_MAX_BATCH / kThreads;   // requests per thread, neighbours
+    static_assert(kPer * kThreads == RKV_MAX_BATCH, "requests divide over the threads");
+    __shared__ int64_t warp_tot[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b0 = threadIdx.x * kPer;
+    int64_t n[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        n[i] = b0 + i < a.batch ? static_cast<int64_t>((request_len(a, b0 + i) + kTile - 1) / kTile) * a.Hkv : 0;
+        sum += n[i];
+    }
+    int64_t v = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        v += lane >= o ? u : 0;
+    }
+    if (lane == 31)
+        warp_tot[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w)
+        v += warp_tot[w];
+    v -= sum;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        v += n[i];
+        if (b0 + i < a.batch)
+            pre[b0 + i + 1] = v;
+    }
+    if (threadIdx.x == 0)
+        pre[0] = 0;
+    __syncthreads();
+}
+
+// CTAs that work: at most one per tile, so that none of them has an empty range.
+__device__ __forceinline__ int workers(int64_t total, int ctas)
+{
+    return static_cast<int>(min(total, static_cast<int64_t>(ctas)));
+}
+
+// CTA p of P takes tiles [first(p), first(p + 1)).
+__device__ __forceinline__ int64_t first_tile(int64_t total, int p, int P) { return total * p / P; }
+
+// The CTA whose range holds tile x.
+__device__ __forceinline__ int owner_of(int64_t total, int64_t x, int P)
+{
+    return static_cast<int>(((x + 1) * P - 1) / total);
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Four codes of a word as two binary16 pairs (bytes 0, 1 and bytes 2, 3), exact.
+template <bool kE4M3>
+__device__ __forceinline__ void to_half(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    if constexpr (kE4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        const uint32_t u = w ^ 0x80808080u;                       // c + 128
+        const uint32_t p = __byte_perm(u, 0x64646464u, 0x4140), q = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&p), off);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&q), off);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
+    }
+}
+
+template <int N>
+struct Piece;                                   // N bytes of a code row
+template <>
+struct Piece<16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const uint8_t* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+};
+template <>
+struct Piece<8> {
+    uint2 v;
+    __device__ __forceinline__ void load(const uint8_t* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+    __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : v.y; }
+};
+
+// The codes of 16 tokens in one lane's registers, and their block's scales.
+template <int D>
+struct Codes {
+    Piece<16> k[2][D / 64];      // tokens g, g + 8; 64 channels each
+    Piece<D / 8> v[4];           // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+    float sk, sv;
+    bool live;
+
+    __device__ __forceinline__ void load(const DecodeArgs& a, int id, int in_block, int kvh, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+        live = id >= 0;
+        if (live) {
+            const int64_t unit = static_cast<int64_t>(id) * a.Hkv + kvh;
+            const int64_t row = (unit << a.block_shift) + in_block;
+            const uint8_t* pk = a.codes_K + row * D;
+            const uint8_t* pv = a.codes_V + row * D;
+            sk = __ldg(a.scale_K + unit);
+            sv = __ldg(a.scale_V + unit);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    k[r][c].load(pk + (g + 8 * r) * D + 64 * c + 16 * t);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r].load(pv + (2 * t + (r & 1) + 8 * (r >> 1)) * D + (D / 8) * g);
+        } else {
+            sk = sv = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    k[r][c].zero();
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r].zero();
+        }
+    }
+};
+
+__device__ __forceinline__ void store_out(void* out, int dtype, int64_t e, float v)
+{
+    if (dtype == RKV_DTYPE_F32)
+        static_cast<float*>(out)[e] = v;
+    else if (dtype == RKV_DTYPE_F16)
+        static_cast<__half*>(out)[e] = __float2half_rn(v);
+    else
+        static_cast<uint16_t*>(out)[e] = f32_to_bf16_bits(v);
+}
+
+// NT: tiles of 8 query heads (G <= 8 * NT).
+template <int D, bool kE4M3, bool kF16, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode_kernel(const DecodeArgs a)
+{
+    constexpr int kSteps = D / 16;               // K-side products per 16 tokens; also V row tiles
+    constexpr int kHeads = 8 * NT;
+    __shared__ int64_t pre[RKV_MAX_BATCH + 1];
+    __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
+    __shared__ float s_o[kWarps][kHeads][D + 4];
+    __shared__ float s_qs[kHeads];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tile_prefix(a, pre);
+    const int64_t total = pre[a.batch];
+    const int p = blockIdx.x, P = workers(total, gridDim.x);
+    int64_t lo = p < P ? first_tile(total, p, P) : 0;
+    const int64_t range_lo = lo, hi = p < P ? first_tile(total, p + 1, P) : 0;
+    bool corrupt = false;
+    if (p == 0)
+        for (int b = tid; b < a.batch; b += kThreads)
+            corrupt |= a.lengths[b] != request_len(a, b);
+
+    while (lo < hi) {
+        // ---- the unit of tile lo and this CTA's part of it
+        int b0 = 0, b1 = a.batch - 1;
+        while (b0 < b1) {
+            const int mid = (b0 + b1 + 1) >> 1;
+            if (pre[mid] <= lo)
+                b0 = mid;
+            else
+                b1 = mid - 1;
+        }
+        const int b = b0, len = request_len(a, b);
+        const int nt = (len + kTile - 1) / kTile;
+        const int kvh = static_cast<int>((lo - pre[b]) / nt);
+        const int64_t u_lo = pre[b] + static_cast<int64_t>(kvh) * nt, u_hi = u_lo + nt;
+        const int t_lo = static_cast<int>(lo - u_lo), t_hi = static_cast<int>(min(hi, u_hi) - u_lo);
+        const int32_t* row = a.table + static_cast<int64_t>(b) * a.max_blocks;
+        const uint16_t* qu = a.q + (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kvh) * a.G) * D;
+
+        // ---- q as B operands: lane (g, t) holds head 8 n + g, the channels of its K pieces
+        uint32_t qf[NT][kSteps][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int head = 8 * n + g;
+            float f[kSteps * 4];
+            float top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int ch = 64 * c + 16 * t + e;
+                    float v = 0.0f;
+                    if (head < a.G) {
+                        if constexpr (kF16)
+                            v = __half2float(__ushort_as_half(qu[head * D + ch]));
+                        else
+                            v = bf16_bits_to_f32(qu[head * D + ch]);
+                    }
+                    f[16 * c + e] = v;
+                    top = fmaxf(top, fabsf(v));
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // q times 2^(15 - e): the largest element in [2^14, 2^15)
+            int e = 15;
+            if (top > 0.0f && top <= FLT_MAX)
+                frexpf(top, &e);
+            const float down = ldexpf(1.0f, 15 - max(-100, e));
+            if (warp == 0 && t == 0)
+                s_qs[head] = a.qk / down;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const __half2 h2 = __floats2half2_rn(f[4 * s + 2 * r] * down, f[4 * s + 2 * r + 1] * down);
+                    qf[n][s][r] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
+        }
+        __syncthreads();
+        float qs[NT][2];                         // logit factors of heads 8 n + 2t, + 1
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            qs[n][0] = s_qs[8 * n + 2 * t];
+            qs[n][1] = s_qs[8 * n + 2 * t + 1];
+        }
+
+        float o[NT][kSteps][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    o[n][i][x] = 0.0f;
+            m[n][0] = m[n][1] = kNone;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+
+        const int tok_mask = (1 << a.block_shift) - 1;
+        for (int ti = t_lo; ti < t_hi; ++ti) {
+            const int tok = ti * kTile + warp * 16;
+            if (tok >= len)
+                break;                           // warp-uniform; only the last tile
+            int id = __ldg(row + (tok >> a.block_shift));
+            if (id < 0 || id >= a.n_blocks) {
+                corrupt = true;
+                id = -1;
+            }
+            Codes<D> c;
+            c.load(a, id, tok & tok_mask, kvh, lane);
+
+            // rows of the block past the request's end may hold anything, NaN codes too
+            if (tok + 16 > len) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (tok + 2 * t + (r & 1) + 8 * (r >> 1) >= len)
+                        c.v[r].zero();
+            }
+
+            // ---- S^T
+            float sc[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                uint32_t af[4];
+                to_half<kE4M3>(c.k[0][s >> 2].word(s & 3), af[0], af[2]);
+                to_half<kE4M3>(c.k[1][s >> 2].word(s & 3), af[1], af[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma16816(sc[n], af, qf[n][s][0], qf[n][s][1]);
+            }
+
+            // ---- weights
+            const bool in0 = c.live && tok + g < len, in1 = c.live && tok + g + 8 < len;
+            const bool sv_ok = c.sv > 0.0f;
+            const float lsv = sv_ok ? __log2f(c.sv) : 0.0f, rsv = sv_ok ? __frcp_rn(c.sv) : 1.0f;
+            uint32_t wf[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float top[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float f = qs[n][x] * c.sk;
+                    sc[n][x] = in0 ? fmaf(sc[n][x], f, lsv) : -INFINITY;
+                    sc[n][2 + x] = in1 ? fmaf(sc[n][2 + x], f, lsv) : -INFINITY;
+                    top[x] = fmaxf(sc[n][x], sc[n][2 + x]);
+                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 4));
+                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 8));
+                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 16));
+                }
+                const float m0 = fmaxf(m[n][0], top[0]), m1 = fmaxf(m[n][1], top[1]);
+                if (__any_sync(0xffffffffu, m0 != m[n][0] || m1 != m[n][1])) {
+                    const float r0 = ex2(m[n][0] - m0), r1 = ex2(m[n][1] - m1);
+                    l[n][0] *= r0;
+                    l[n][1] *= r1;
+#pragma unroll
+                    for (int i = 0; i < kSteps; ++i) {
+                        o[n][i][0] *= r0;
+                        o[n][i][1] *= r1;
+                        o[n][i][2] *= r0;
+                        o[n][i][3] *= r1;
+                    }
+                    m[n][0] = m0;
+                    m[n][1] = m1;
+                }
+                const float b0 = kWeightExp - m0, b1 = kWeightExp - m1;
+                const float w00 = ex2(sc[n][0] + b0), w01 = ex2(sc[n][1] + b1);
+                const float w10 = ex2(sc[n][2] + b0), w11 = ex2(sc[n][3] + b1);
+                l[n][0] = fmaf(w00 + w10, rsv, l[n][0]);
+                l[n][1] = fmaf(w01 + w11, rsv, l[n][1]);
+                const __half2 p0 = __floats2half2_rn(w00, w01), p1 = __floats2half2_rn(w10, w11);
+                wf[n][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
+                wf[n][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+            }
+
+            // ---- O^T: bytes of tokens 2t and 2t + 1 interleaved into pairs, two row tiles per 2 channels
+#pragma unroll
+            for (int j = 0; j < kSteps / 2; ++j) {
+                uint32_t lo4[2], hi4[2];         // channels 4j, 4j+1 and 4j+2, 4j+3 of both tokens of a pair
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    lo4[r] = __byte_perm(c.v[2 * r].word(j), c.v[2 * r + 1].word(j), 0x5140);
+                    hi4[r] = __byte_perm(c.v[2 * r].word(j), c.v[2 * r + 1].word(j), 0x7362);
+                }
+                uint32_t af[4];
+                to_half<kE4M3>(lo4[0], af[0], af[1]);
+                to_half<kE4M3>(lo4[1], af[2], af[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma16816(o[n][2 * j], af, wf[n][0], wf[n][1]);
+                to_half<kE4M3>(hi4[0], af[0], af[1]);
+                to_half<kE4M3>(hi4[1], af[2], af[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma16816(o[n][2 * j + 1], af, wf[n][0], wf[n][1]);
+            }
+        }
+
+        // ---- merge the warps
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float v = l[n][x];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (g == 0) {
+                    s_m[warp][8 * n + 2 * t + x] = m[n][x];
+                    s_l[warp][8 * n + 2 * t + x] = v;
+                }
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    // rows g and g + 8 of row tile i: channels (D / 8) g + 2 i, + 1
+                    s_o[warp][8 * n + 2 * t + x][(D / 8) * g + 2 * i] = o[n][i][x];
+                    s_o[warp][8 * n + 2 * t + x][(D / 8) * g + 2 * i + 1] = o[n][i][2 + x];
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = t_lo == 0 && t_hi == nt;
+        const bool head_part = lo == range_lo && t_lo > 0;   // began in an earlier CTA
+        float* part = a.parts + static_cast<int64_t>(2 * p + (head_part ? 0 : 1)) * a.G * (D + 2);
+        for (int x = tid; x < a.G * D; x += kThreads) {
+            const int head = x / D, ch = x % D;
+            float M = kNone;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                M = fmaxf(M, s_m[w][head]);
+            float L = 0.0f, O = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(s_m[w][head] - M);
+                L = fmaf(s_l[w][head], f, L);
+                O = fmaf(s_o[w][head][ch], f, O);
+            }
+            if (whole) {
+                store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
+                          L > 0.0f ? O / L : 0.0f);
+            } else {
+                part[head * (D + 2) + ch] = O;
+                if (ch == 0) {
+                    part[head * (D + 2) + D] = M;
+                    part[head * (D + 2) + D + 1] = L;
+                }
+            }
+        }
+        __syncthreads();
+        lo = u_lo + t_hi;
+    }
+    if (__any_sync(0xffffffffu, corrupt) && lane == 0)
+        report(a.err, RKV_ERR_CORRUPT);
+}
+
+// Joins the parts of the units that more than one CTA worked on, in CTA order; zeros for empty requests.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, int ctas)
+{
+    __shared__ int64_t pre[RKV_MAX_BATCH + 1];
+    const int b = blockIdx.x, kvh = blockIdx.y, tid = threadIdx.x;
+    tile_prefix(a, pre);
+    const int64_t total = pre[a.batch];
+    const int P = workers(total, ctas);
+    const int64_t nt = (pre[b + 1] - pre[b]) / a.Hkv;
+    const int64_t u_lo = pre[b] + kvh * nt, u_hi = u_lo + nt;
+    const int pa = nt ? owner_of(total, u_lo, P) : 0, pb = nt ? owner_of(total, u_hi - 1, P) : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (nt && pa == pb)
+        return;
+    for (int x = tid; x < a.G * D; x += kThreads) {
+        const int head = x / D, ch = x % D;
+        float M = kNone, L = 0.0f, O = 0.0f;
+        for (int p = pa; nt && p <= pb; ++p) {
+            const float* part = a.parts + (static_cast<int64_t>(2 * p + (p == pa ? 1 : 0)) * a.G + head) * (D + 2);
+            const float pm = __ldcg(part + D), pl = __ldcg(part + D + 1), po = __ldcg(part + ch);
+            const float n = fmaxf(M, pm), f = ex2(M - n), e = ex2(pm - n);
+            L = fmaf(L, f, pl * e);
+            O = fmaf(O, f, po * e);
+            M = n;
+        }
+        store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
+                  L > 0.0f ? O / L : 0.0f);
+    }
+}
+
+template <int D, bool kE4M3, bool kF16>
+cudaError_t launch_t(const DecodeArgs& a, int ctas, cudaStream_t st)
+{
+    if (a.G <= 8)
+        kv8_decode_kernel<D, kE4M3, kF16, 1><<<ctas, kThreads, 0, st>>>(a);
+    else
+        kv8_decode_kernel<D, kE4M3, kF16, 2><<<ctas, kThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.batch, a.Hkv);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D>, a, ctas);
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeArgs& a, bool e4m3, bool f16, int ctas, cudaStream_t st)
+{
+    if (e4m3)
+        return f16 ? launch_t<D, true, true>(a, ctas, st) : launch_t<D, true, false>(a, ctas, st);
+    return f16 ? launch_t<D, false, true>(a, ctas, st) : launch_t<D, false, false>(a, ctas, st);
+}
+
+// CTAs of a launch: what the SMs hold at once (the NT = 2 form holds two per SM), at most one per tile
+// that the table could hold.
+int decode_ctas(const rkv_kv8_cache& c, int sms)
+{
+    const int per_sm = c.n_q_heads / c.n_kv_heads <= 8 ? kCtasPerSm : 2;
+    const int64_t tiles = static_cast<int64_t>(c.batch) * c.n_kv_heads *
+                          ((static_cast<int64_t>(c.max_blocks) * c.block_size + kTile - 1) / kTile);
+    return static_cast<int>(tiles < per_sm * sms ? tiles : per_sm * sms);
+}
+
+}  // namespace
+
+uint64_t kv8_decode_ws_bytes(const rkv_kv8_cache& c, int sms)
+{
+    const uint64_t G = c.n_q_heads / c.n_kv_heads;
+    return 2ull * decode_ctas(c, sms) * G * (c.head_dim + 2) * 4;
+}
+
+cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32_t* table, const int32_t* lengths,
+                              void* out, void* workspace, int sms, cudaStream_t st)
+{
+    DecodeArgs a;
+    a.Hkv = c.n_kv_heads;
+    a.Hq = c.n_q_heads;
+    a.G = c.n_q_heads / c.n_kv_heads;
+    a.batch = c.batch;
+    a.block_shift = 0;
+    while ((1 << a.block_shift) < c.block_size)
+        ++a.block_shift;
+    a.n_blocks = c.n_blocks;
+    a.max_blocks = c.max_blocks;
+    a.out_dtype = c.out_dtype;
+    const double scale = c.scale > 0.0f ? c.scale : 1.0 / std::sqrt(static_cast<double>(c.head_dim));
+    a.qk = static_cast<float>(scale * 1.4426950408889634);
+    a.q = static_cast<const uint16_t*>(q);
+    a.codes_K = c.codes_K;
+    a.codes_V = c.codes_V;
+    a.scale_K = c.scale_K;
+    a.scale_V = c.scale_V;
+    a.table = table;
+    a.lengths = lengths;
+    a.out = out;
+    a.parts = static_cast<float*>(workspace);
+    a.err = c.device_status;
+    const bool e4m3 = c.code_type == RKV_KV8_E4M3, f16 = c.in_dtype == RKV_DTYPE_F16;
+    const int ctas = decode_ctas(c, sms);
+    return c.head_dim == 128 ? launch_d<128>(a, e4m3, f16, ctas, st) : launch_d<64>(a, e4m3, f16, ctas, st);
+}
+
+}  // namespace rkv

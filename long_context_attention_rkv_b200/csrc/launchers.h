@@ -67,6 +67,26 @@ cudaError_t launch_decode_mma(const CacheArgs& a, int64_t ref_rows, int64_t cmp_
 cudaError_t launch_decode_combine(const CacheArgs& a, int batch, int splits, const float* partials, void* out,
                                   cudaStream_t st);
 
+// Block tables (kernels_blocks.cu) and the 8-bit block cache (kernels_kv8_*.cu); arguments are
+// those of the entry points in rkv.h, already checked.
+cudaError_t launch_blocks_extend(const rkv_blocks_config& c, const int32_t* lengths, const int32_t* new_counts,
+                                 int32_t* table, const int32_t* free_list, const int32_t* n_free, int32_t* new_off,
+                                 int32_t* slot_map, int64_t max_new, int32_t* lengths_out, int32_t* n_free_out,
+                                 int32_t* err, cudaStream_t st);
+cudaError_t launch_blocks_release(const rkv_blocks_config& c, const int32_t* lengths, const int32_t* ended,
+                                  const int32_t* table, int32_t* free_list, const int32_t* n_free,
+                                  int32_t* lengths_out, int32_t* n_free_out, int32_t* err, cudaStream_t st);
+cudaError_t launch_kv8_store(const rkv_kv8_cache& c, const void* K_new, const void* V_new, int64_t row_stride,
+                             int64_t head_stride, const int32_t* slots, int64_t n_rows, cudaStream_t st);
+uint64_t kv8_decode_ws_bytes(const rkv_kv8_cache& c, int sms);
+cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32_t* table, const int32_t* lengths,
+                              void* out, void* workspace, int sms, cudaStream_t st);
+
+// Causal attention of packed prompts (kernels_prefill.cu).
+cudaError_t launch_prefill(const rkv_prefill_config& c, const void* q, const void* K, const void* V,
+                           const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_len, void* out, float* lse,
+                           int32_t* err, int sms, cudaStream_t st);
+
 // Self-test of the bounded waits: records RKV_ERR_TIMEOUT in *err after one wait gives up.
 cudaError_t launch_wait_timeout_selftest(int32_t* err, cudaStream_t st);
 
