@@ -302,47 +302,56 @@ def rkv_selftest_wait_timeout(err_dev, stream=None):
     _check(lib().rkv_selftest_wait_timeout(_ptr(err_dev), _stream(stream)), "rkv_selftest_wait_timeout")
 
 
-def _same_device(where: str, *tensors):
-    """Tensors of another device than the current one (whose stream the call uses) are refused."""
+def _refuse(where: str, why: str):
+    raise RkvError(STATUS_CODE["RKV_ERR_INVALID_ARG"], f"{where} ({why})")
+
+
+def _local(where: str, tensors):
+    """Device addresses of tensors (None and plain addresses pass) and the current device's ordinal; tensors of
+    another device, whose streams the call would not follow, are refused."""
     import torch
 
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()
+    out = []
     for x in tensors:
-        if x is not None and hasattr(x, "get_device") and x.get_device() != cur:
-            raise RkvError(STATUS_CODE["RKV_ERR_INVALID_ARG"], f"{where}: a tensor on {x.device}, not on cuda:{cur}")
+        if isinstance(x, torch.Tensor):
+            if x.get_device() != cur:
+                _refuse(where, f"a tensor on {x.device}, not on cuda:{cur}")
+            out.append(x.data_ptr())
+        else:
+            out.append(x)
+    return out, cur
+
+
+def _raw_stream(stream, cur: int) -> int:
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
 
 
 def rkv_prefill_attn(cfg: rkv_prefill_config, q, K, V, q_off, kv_off, kv_len, out, lse, device_status, stream=None):
-    _same_device("rkv_prefill_attn", q, K, V, q_off, kv_off, kv_len, out, lse, device_status)
-    _check(lib().rkv_prefill_attn(ctypes.addressof(cfg), _ptr(q), _ptr(K), _ptr(V), _ptr(q_off), _ptr(kv_off),
-                                  _ptr(kv_len), _ptr(out), _ptr(lse), _ptr(device_status), _stream(stream)),
-           "rkv_prefill_attn")
+    p, cur = _local("rkv_prefill_attn", (q, K, V, q_off, kv_off, kv_len, out, lse, device_status))
+    _check(lib().rkv_prefill_attn(ctypes.addressof(cfg), *p, _raw_stream(stream, cur)), "rkv_prefill_attn")
 
 
 def rkv_blocks_extend(cfg: rkv_blocks_config, lengths, new_counts, block_table, free_list, n_free, new_off, slot_map,
                       max_new: int, lengths_out, n_free_out, device_status, stream=None):
-    _same_device("rkv_blocks_extend", lengths, new_counts, block_table, free_list, n_free, new_off, slot_map,
-                 lengths_out, n_free_out, device_status)
-    _check(lib().rkv_blocks_extend(ctypes.addressof(cfg), _ptr(lengths), _ptr(new_counts), _ptr(block_table),
-                                   _ptr(free_list), _ptr(n_free), _ptr(new_off), _ptr(slot_map), max_new,
-                                   _ptr(lengths_out), _ptr(n_free_out), _ptr(device_status), _stream(stream)),
-           "rkv_blocks_extend")
+    p, cur = _local("rkv_blocks_extend", (lengths, new_counts, block_table, free_list, n_free, new_off, slot_map,
+                                          max_new, lengths_out, n_free_out, device_status))
+    _check(lib().rkv_blocks_extend(ctypes.addressof(cfg), *p, _raw_stream(stream, cur)), "rkv_blocks_extend")
 
 
 def rkv_blocks_release(cfg: rkv_blocks_config, lengths, ended, block_table, free_list, n_free, lengths_out, n_free_out,
                        device_status, stream=None):
-    _same_device("rkv_blocks_release", lengths, ended, block_table, free_list, n_free, lengths_out, n_free_out,
-                 device_status)
-    _check(lib().rkv_blocks_release(ctypes.addressof(cfg), _ptr(lengths), _ptr(ended), _ptr(block_table),
-                                    _ptr(free_list), _ptr(n_free), _ptr(lengths_out), _ptr(n_free_out),
-                                    _ptr(device_status), _stream(stream)), "rkv_blocks_release")
+    p, cur = _local("rkv_blocks_release", (lengths, ended, block_table, free_list, n_free, lengths_out, n_free_out,
+                                           device_status))
+    _check(lib().rkv_blocks_release(ctypes.addressof(cfg), *p, _raw_stream(stream, cur)), "rkv_blocks_release")
 
 
 def rkv_kv8_store(cache: rkv_kv8_cache, K_new, V_new, row_stride: int, head_stride: int, slot_map, n_rows: int,
                   stream=None):
-    _same_device("rkv_kv8_store", K_new, V_new, slot_map)
-    _check(lib().rkv_kv8_store(ctypes.addressof(cache), _ptr(K_new), _ptr(V_new), row_stride, head_stride,
-                               _ptr(slot_map), n_rows, _stream(stream)), "rkv_kv8_store")
+    p, cur = _local("rkv_kv8_store", (K_new, V_new, row_stride, head_stride, slot_map, n_rows))
+    _check(lib().rkv_kv8_store(ctypes.addressof(cache), *p, _raw_stream(stream, cur)), "rkv_kv8_store")
 
 
 def rkv_kv8_workspace(cache: rkv_kv8_cache) -> int:
@@ -353,9 +362,8 @@ def rkv_kv8_workspace(cache: rkv_kv8_cache) -> int:
 
 def rkv_kv8_decode_attn(cache: rkv_kv8_cache, q, block_table, lengths, out, workspace, workspace_bytes: int,
                         stream=None):
-    _same_device("rkv_kv8_decode_attn", q, block_table, lengths, out, workspace)
-    _check(lib().rkv_kv8_decode_attn(ctypes.addressof(cache), _ptr(q), _ptr(block_table), _ptr(lengths), _ptr(out),
-                                     _ptr(workspace), workspace_bytes, _stream(stream)), "rkv_kv8_decode_attn")
+    p, cur = _local("rkv_kv8_decode_attn", (q, block_table, lengths, out, workspace, workspace_bytes))
+    _check(lib().rkv_kv8_decode_attn(ctypes.addressof(cache), *p, _raw_stream(stream, cur)), "rkv_kv8_decode_attn")
 
 
 # --- buffers ---------------------------------------------------------------------------
@@ -418,10 +426,6 @@ class Layer:
 
     def unit(self, seq: int, kv_head: int) -> rkv_unit_view:
         return rkv_unit_view_get(self.desc, seq, kv_head)
-
-
-def _refuse(where: str, why: str):
-    raise RkvError(STATUS_CODE["RKV_ERR_INVALID_ARG"], f"{where} ({why})")
 
 
 def _take_error(status) -> int:
@@ -507,7 +511,7 @@ class KV8Cache:
         if workspace is None:
             workspace = torch.empty(max(256, self.ws_bytes), dtype=torch.uint8, device=device)
         self.workspace = workspace
-        _same_device("KV8Cache", self.codes_K, self.codes_V, self.scale_K, self.scale_V, self.workspace)
+        _local("KV8Cache", (self.codes_K, self.codes_V, self.scale_K, self.scale_V, self.workspace))
         self.c = rkv_kv8_cache.from_buffer_copy(cfg)
         for name in ("codes_K", "codes_V", "scale_K", "scale_V"):
             setattr(self.c, name, getattr(self, name).data_ptr())

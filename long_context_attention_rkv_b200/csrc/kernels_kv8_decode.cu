@@ -47,7 +47,8 @@ using namespace kv8;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;     // tokens per CTA step
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
+constexpr int kMaxCtas = 160 * kCtasPerSm;
 constexpr float kNone = -1e30f;        // running maximum before any token
 constexpr float kWeightExp = 15.0f;    // weights are kept times 2^15: binary16 then holds 2^-39 .. 1 of the largest
 
@@ -62,7 +63,8 @@ struct DecodeArgs {
     const int32_t* table;
     const int32_t* lengths;
     void* out;
-    float* parts;                      // [2 * CTAs][heads][D + 2]
+    float* part_o;                     // [2 * CTAs][heads][D]
+    float2* part_ml;                   // [2 * CTAs][heads]: M, L
     int32_t* err;
 };
 
@@ -189,38 +191,30 @@ struct Codes {
     Piece<16> k[2][D / 64];      // tokens g, g + 8; 64 channels each
     Piece<D / 8> v[4];           // tokens 2t, 2t + 1, 2t + 8, 2t + 9
     float sk, sv;
-    bool live;
 
-    __device__ __forceinline__ void load(const DecodeArgs& a, int id, int in_block, int kvh, int lane)
+    // id < 0: a block outside the pool, skipped by its logits; any block of the pool stands in for its rows
+    __device__ __forceinline__ void load_k(const DecodeArgs& a, int id, int in_block, int kvh, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
-        live = id >= 0;
-        if (live) {
-            const int64_t unit = static_cast<int64_t>(id) * a.Hkv + kvh;
-            const int64_t row = (unit << a.block_shift) + in_block;
-            const uint8_t* pk = a.codes_K + row * D;
-            const uint8_t* pv = a.codes_V + row * D;
-            sk = __ldg(a.scale_K + unit);
-            sv = __ldg(a.scale_V + unit);
+        const int64_t unit = static_cast<int64_t>(max(id, 0)) * a.Hkv + kvh;
+        const uint8_t* p = a.codes_K + ((unit << a.block_shift) + in_block) * D;
+        sk = __ldg(a.scale_K + unit);
+        sv = __ldg(a.scale_V + unit);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    k[r][c].load(pk + (g + 8 * r) * D + 64 * c + 16 * t);
+            for (int c = 0; c < D / 64; ++c)
+                k[r][c].load(p + (g + 8 * r) * D + 64 * c + 16 * t);
+    }
+
+    __device__ __forceinline__ void load_v(const DecodeArgs& a, int id, int in_block, int kvh, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+        const int64_t unit = static_cast<int64_t>(max(id, 0)) * a.Hkv + kvh;
+        const uint8_t* p = a.codes_V + ((unit << a.block_shift) + in_block) * D;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                v[r].load(pv + (2 * t + (r & 1) + 8 * (r >> 1)) * D + (D / 8) * g);
-        } else {
-            sk = sv = 0.0f;
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    k[r][c].zero();
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                v[r].zero();
-        }
+        for (int r = 0; r < 4; ++r)
+            v[r].load(p + (2 * t + (r & 1) + 8 * (r >> 1)) * D + (D / 8) * g);
     }
 };
 
@@ -335,24 +329,37 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             l[n][0] = l[n][1] = 0.0f;
         }
 
+        // This warp's 16 tokens of each tile.  The next tile's K codes are loaded as soon as this one's are in
+        // the products, its V codes likewise, and its block id a tile earlier: loads stay in flight all
+        // the time without a second set of registers.
         const int tok_mask = (1 << a.block_shift) - 1;
+        auto block_id = [&](int ti) {
+            const int tok = ti * kTile + warp * 16;
+            return tok < len && ti < t_hi ? __ldg(row + (tok >> a.block_shift)) : 0;
+        };
+        auto checked = [&](int id) {
+            const bool bad = id < 0 || id >= a.n_blocks;
+            corrupt |= bad;
+            return bad ? -1 : id;
+        };
+        Codes<D> c;
+        int id = checked(block_id(t_lo)), next_id = block_id(t_lo + 1);
+        c.load_k(a, id, (t_lo * kTile + warp * 16) & tok_mask, kvh, lane);
+        c.load_v(a, id, (t_lo * kTile + warp * 16) & tok_mask, kvh, lane);
         for (int ti = t_lo; ti < t_hi; ++ti) {
             const int tok = ti * kTile + warp * 16;
             if (tok >= len)
                 break;                           // warp-uniform; only the last tile
-            int id = __ldg(row + (tok >> a.block_shift));
-            if (id < 0 || id >= a.n_blocks) {
-                corrupt = true;
-                id = -1;
-            }
-            Codes<D> c;
-            c.load(a, id, tok & tok_mask, kvh, lane);
+            const bool live = id >= 0;
+            id = checked(next_id);
+            next_id = block_id(ti + 2);
+            const int next_row = (tok + kTile) & tok_mask;
 
             // rows of the block past the request's end may hold anything, NaN codes too
-            if (tok + 16 > len) {
+            if (tok + 16 > len || !live) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (tok + 2 * t + (r & 1) + 8 * (r >> 1) >= len)
+                    if (!live || tok + 2 * t + (r & 1) + 8 * (r >> 1) >= len)
                         c.v[r].zero();
             }
 
@@ -372,16 +379,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             }
 
             // ---- weights
-            const bool in0 = c.live && tok + g < len, in1 = c.live && tok + g + 8 < len;
-            const bool sv_ok = c.sv > 0.0f;
-            const float lsv = sv_ok ? __log2f(c.sv) : 0.0f, rsv = sv_ok ? __frcp_rn(c.sv) : 1.0f;
+            const float sk = c.sk, sv = c.sv;
+            c.load_k(a, id, next_row, kvh, lane);
+            const bool in0 = live && tok + g < len, in1 = live && tok + g + 8 < len;
+            const bool sv_ok = sv > 0.0f;
+            const float lsv = sv_ok ? __log2f(sv) : 0.0f, rsv = sv_ok ? __frcp_rn(sv) : 1.0f;
             uint32_t wf[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float top[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float f = qs[n][x] * c.sk;
+                    const float f = qs[n][x] * sk;
                     sc[n][x] = in0 ? fmaf(sc[n][x], f, lsv) : -INFINITY;
                     sc[n][2 + x] = in1 ? fmaf(sc[n][2 + x], f, lsv) : -INFINITY;
                     top[x] = fmaxf(sc[n][x], sc[n][2 + x]);
@@ -435,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                 for (int n = 0; n < NT; ++n)
                     mma16816(o[n][2 * j + 1], af, wf[n][0], wf[n][1]);
             }
+            c.load_v(a, id, next_row, kvh, lane);
         }
 
         // ---- merge the warps
@@ -461,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
         __syncthreads();
         const bool whole = t_lo == 0 && t_hi == nt;
         const bool head_part = lo == range_lo && t_lo > 0;   // began in an earlier CTA
-        float* part = a.parts + static_cast<int64_t>(2 * p + (head_part ? 0 : 1)) * a.G * (D + 2);
+        const int64_t part = static_cast<int64_t>(2 * p + (head_part ? 0 : 1)) * a.G;
         for (int x = tid; x < a.G * D; x += kThreads) {
             const int head = x / D, ch = x % D;
             float M = kNone;
@@ -479,11 +489,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                 store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
                           L > 0.0f ? O / L : 0.0f);
             } else {
-                part[head * (D + 2) + ch] = O;
-                if (ch == 0) {
-                    part[head * (D + 2) + D] = M;
-                    part[head * (D + 2) + D + 1] = L;
-                }
+                a.part_o[(part + head) * D + ch] = O;
+                if (ch == 0)
+                    a.part_ml[part + head] = make_float2(M, L);
             }
         }
         __syncthreads();
@@ -493,34 +501,74 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
         report(a.err, RKV_ERR_CORRUPT);
 }
 
-// Joins the parts of the units that more than one CTA worked on, in CTA order; zeros for empty requests.
+// Joins the parts of a unit that more than one CTA worked on, in a fixed order; zeros for empty requests.  One CTA
+// per query head: the parts' factors first (all their maxima at once), then the weighted sum with a warp per part.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, int ctas)
 {
+    constexpr int kLanes = D / 4;                        // lanes of a row, four channels each
+    constexpr int kRows = kThreads / kLanes;             // parts in flight per round
     __shared__ int64_t pre[RKV_MAX_BATCH + 1];
-    const int b = blockIdx.x, kvh = blockIdx.y, tid = threadIdx.x;
+    __shared__ float s_f[kMaxCtas], s_r[2][kWarps];
+    __shared__ float4 s_o[kRows][kLanes];
+    const int b = blockIdx.x, kvh = blockIdx.y / a.G, head = blockIdx.y % a.G, tid = threadIdx.x;
     tile_prefix(a, pre);
     const int64_t total = pre[a.batch];
     const int P = workers(total, ctas);
     const int64_t nt = (pre[b + 1] - pre[b]) / a.Hkv;
     const int64_t u_lo = pre[b] + kvh * nt, u_hi = u_lo + nt;
-    const int pa = nt ? owner_of(total, u_lo, P) : 0, pb = nt ? owner_of(total, u_hi - 1, P) : 0;
+    const int pa = nt ? owner_of(total, u_lo, P) : 0, pb = nt ? owner_of(total, u_hi - 1, P) : -1;
+    const int np = pb - pa + 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (nt && pa == pb)
+    if (np == 1)
         return;
-    for (int x = tid; x < a.G * D; x += kThreads) {
-        const int head = x / D, ch = x % D;
-        float M = kNone, L = 0.0f, O = 0.0f;
-        for (int p = pa; nt && p <= pb; ++p) {
-            const float* part = a.parts + (static_cast<int64_t>(2 * p + (p == pa ? 1 : 0)) * a.G + head) * (D + 2);
-            const float pm = __ldcg(part + D), pl = __ldcg(part + D + 1), po = __ldcg(part + ch);
-            const float n = fmaxf(M, pm), f = ex2(M - n), e = ex2(pm - n);
-            L = fmaf(L, f, pl * e);
-            O = fmaf(O, f, po * e);
-            M = n;
-        }
-        store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
-                  L > 0.0f ? O / L : 0.0f);
+    // part i: the unit's first CTA left its tail slot, the others their head slots
+    auto slot = [&](int i) { return (static_cast<int64_t>(2 * (pa + i)) + (i == 0 ? 1 : 0)) * a.G + head; };
+    float M = kNone;
+    for (int i = tid; i < np; i += kThreads)
+        M = fmaxf(M, __ldcg(&a.part_ml[slot(i)]).x);
+    M = warp_max(M);
+    if ((tid & 31) == 0)
+        s_r[0][tid >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        M = fmaxf(M, s_r[0][w]);
+    float L = 0.0f;
+    for (int i = tid; i < np; i += kThreads) {
+        const float2 ml = __ldcg(&a.part_ml[slot(i)]);
+        const float f = ex2(ml.x - M);
+        s_f[i] = f;
+        L = fmaf(ml.y, f, L);
+    }
+    L = warp_sum(L);
+    if ((tid & 31) == 0)
+        s_r[1][tid >> 5] = L;
+    __syncthreads();
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        L += s_r[1][w];
+    const int row = tid / kLanes, col = tid % kLanes;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = row; i < np; i += kRows) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D) + col);
+        const float f = s_f[i];
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+    }
+    s_o[row][col] = o;
+    __syncthreads();
+    if (tid < D) {
+        float v = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            v += reinterpret_cast<const float*>(s_o[r])[tid];
+        store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + tid,
+                  L > 0.0f ? v / L : 0.0f);
     }
 }
 
@@ -535,7 +583,7 @@ cudaError_t launch_t(const DecodeArgs& a, int ctas, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.batch, a.Hkv);
+    cfg.gridDim = dim3(a.batch, a.Hq);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -569,7 +617,7 @@ int decode_ctas(const rkv_kv8_cache& c, int sms)
 uint64_t kv8_decode_ws_bytes(const rkv_kv8_cache& c, int sms)
 {
     const uint64_t G = c.n_q_heads / c.n_kv_heads;
-    return 2ull * decode_ctas(c, sms) * G * (c.head_dim + 2) * 4;
+    return 2ull * decode_ctas(c, sms) * G * (c.head_dim * 4 + 8);
 }
 
 cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32_t* table, const int32_t* lengths,
@@ -596,10 +644,11 @@ cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32
     a.table = table;
     a.lengths = lengths;
     a.out = out;
-    a.parts = static_cast<float*>(workspace);
     a.err = c.device_status;
     const bool e4m3 = c.code_type == RKV_KV8_E4M3, f16 = c.in_dtype == RKV_DTYPE_F16;
     const int ctas = decode_ctas(c, sms);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + 2ll * ctas * a.G * c.head_dim);
     return c.head_dim == 128 ? launch_d<128>(a, e4m3, f16, ctas, st) : launch_d<64>(a, e4m3, f16, ctas, st);
 }
 

@@ -9,10 +9,17 @@
 // at most s'/2 + s'/4 + ... < s', however many tokens the block receives one by one.
 //
 // Bound by HBM: 2 bytes read and 1 written per element.  One CTA does the K or the V side of the runs
-// that start in one window of packed rows, for one head; it holds a run (at most 128 rows) in registers
-// between the maximum and the codes, so the rows are read once.  A window is one block's worth of rows
-// for prompts (then it holds about one run) and a single row for decode steps (every row is a run of
-// its own and all of them go side by side).
+// that start in one window of packed rows, for one head; it holds a run (at most one block of rows) in
+// registers between the maximum and the codes, so the rows are read once.  A window is one block's worth of
+// rows for prompts (then it holds about one run) and a single row for decode steps (every row is a run of
+// its own and all of them go side by side).  The CTA has block * head_dim / 64 threads, so that each holds
+// eight 16-byte pieces of a full block: small CTAs, many of them per SM, keep loads in flight while others
+// reduce and convert.
+//
+// The quotient x / s decides the code through its rounding, so it must be the correctly rounded one; but
+// x * fl(1 / s) is within 3 half steps (2^-22.4) of x / s, so the rounding can only differ if that product
+// lies within 2^-20 (relative) of a border between two codes.  Only then (and in the floats' subnormal
+// range) is the division done.
 #include <cfloat>
 
 #include "kv8_common.cuh"
@@ -24,11 +31,10 @@ namespace {
 
 using namespace kv8;
 
-constexpr int kThreads = 256;
 constexpr int kMaxBlock = 128;
 
 struct StoreArgs {
-    int32_t Hkv, block, n_blocks, window;
+    int32_t Hkv, shift, n_blocks, window;
     int64_t row_stride, head_stride, n_rows;
     const uint16_t* x[2];
     uint8_t* codes[2];
@@ -55,9 +61,14 @@ __device__ __forceinline__ void widen(const uint4& v, float (&f)[8])
 }
 
 // Largest bit pattern of |x| over the CTA (non-negative floats order as their bits).
+template <int kThreads>
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red)
 {
     v = __reduce_max_sync(0xffffffffu, v);
+    if constexpr (kThreads == 32) {
+        __syncwarp();
+        return v;
+    }
     __syncthreads();   // the previous round's values have been read
     if ((threadIdx.x & 31) == 0)
         red[threadIdx.x >> 5] = v;
@@ -69,43 +80,114 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red)
     return m;
 }
 
-template <int D, bool kE4M3, bool kF16>
-__global__ void __launch_bounds__(kThreads) kv8_store_kernel(const StoreArgs a)
+// Eight codes of x / s: r = fl(1 / s); exact: every quotient by division.
+template <bool kE4M3>
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, float r, bool exact)
+{
+    uint32_t o[2];
+    float t[8];
+    if constexpr (kE4M3) {
+        // border between two normal codes: the 20 bits under the three kept ones are 0x80000
+        uint32_t dist = 0xffffffffu;
+        float small = FLT_MAX;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            t[e] = __fmul_rn(x[e], r);
+            dist = min(dist, (__float_as_uint(t[e]) - 0x7fff8u) & 0xfffffu);
+            small = fminf(small, fabsf(t[e]));
+        }
+        exact |= dist <= 16u || small < 0x1p-6f;
+    } else {
+        // t + 1.5 2^23 holds rint(t) in its low bits
+        float far = 0.0f;
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            t[e] = __fmul_rn(x[e], r);
+            const float m = __fadd_rn(t[e], 12582912.0f);
+            far = fmaxf(far, fabsf(t[e] - (m - 12582912.0f)));
+            u[e] = __float_as_uint(m);
+        }
+        exact |= far > 0.5f - 0x1p-14f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            o[i] = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040), __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040),
+                               0x5410);
+    }
+    if (exact) {
+        o[0] = o[1] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            o[e >> 2] |= encode<kE4M3>(__fdiv_rn(x[e], s)) << (8 * (e & 3));
+    } else if constexpr (kE4M3) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i], t[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i + 2], t[4 * i + 3]), __NV_SATFINITE,
+                                                         __NV_E4M3);
+            o[i] = lo | (hi << 16);
+        }
+    }
+    return make_uint2(o[0], o[1]);
+}
+
+// A word of two 16-bit values: the largest finite magnitude, NaN turned into 0.
+__device__ __forceinline__ void clean(uint32_t& w, uint32_t& top, uint32_t inf)
+{
+    const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+    top = max(top, max(lo < inf ? lo : 0u, hi < inf ? hi : 0u));
+    w = (lo > inf ? 0u : w & 0xffffu) | (hi > inf ? 0u : w & 0xffff0000u);
+}
+
+// Smallest m >= 0 with was * 2^m >= need; 0 < was < need, both normal.
+__device__ __forceinline__ int doublings(float was, float need)
+{
+    const uint32_t w = __float_as_uint(was), n = __float_as_uint(need);
+    return static_cast<int>(n >> 23) - static_cast<int>(w >> 23) + ((n & 0x7fffffu) > (w & 0x7fffffu) ? 1 : 0);
+}
+
+// 2^e for e in [-126, 127]; 0 below.
+__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+template <int D, int kThreads, bool kE4M3, bool kF16>
+__global__ void __launch_bounds__(kThreads, 768 / kThreads) kv8_store_kernel(const StoreArgs a)
 {
     constexpr int kCols = D / 8;                                   // 16-byte pieces of an input row
-    constexpr int kPieces = kMaxBlock * kCols / kThreads;          // per thread, for a run of 128 rows
-    __shared__ int sl[kThreads + 1];                               // slots of the rows from w0 - 1 on
-    __shared__ uint32_t starts[kThreads / 32], goes_on[kThreads / 32];
+    constexpr int kPieces = 8;                                     // per thread, for a full block
+    constexpr int kSlots = 2 * kMaxBlock;
+    __shared__ int sl[kSlots + 1];                                 // slots of the rows from w0 - 1 on
+    __shared__ uint32_t starts[kSlots / 32], goes_on[kSlots / 32];
     __shared__ uint32_t red[kThreads / 32];
 
     const int tid = threadIdx.x, side = blockIdx.y;
     const int h = blockIdx.x % a.Hkv;
     const int64_t w0 = static_cast<int64_t>(blockIdx.x / a.Hkv) * a.window;
-    const int mask = a.block - 1;
-    const int64_t pool = static_cast<int64_t>(a.n_blocks) * a.block;
+    const int mask = (1 << a.shift) - 1, near = a.window + mask + 1;
+    const int64_t pool = static_cast<int64_t>(a.n_blocks) << a.shift;
 
     // ---- the runs that start in this window
     bool corrupt = false;
-    for (int i = tid; i <= a.window + a.block; i += kThreads) {
+    for (int i = tid; i <= near; i += kThreads) {
         const int64_t r = w0 - 1 + i;
         int v = (r >= 0 && r < a.n_rows) ? a.slots[r] : -1;
         if (v >= pool) {
             corrupt = true;
             v = -1;
         }
-        if (i <= kThreads)
-            sl[i] = v < 0 ? -2 : v;   // -2: no row follows it as its next slot
+        sl[i] = v < 0 ? -2 : v;   // -2: no row follows it as its next slot
     }
     if (corrupt)
         report(a.err, RKV_ERR_CORRUPT);
     __syncthreads();
-    const bool near = tid < a.window + a.block;
-    const bool on = near && sl[tid + 1] > 0 && sl[tid + 1] == sl[tid] + 1 && (sl[tid + 1] & mask) != 0;
-    const bool start = tid < a.window && sl[tid + 1] >= 0 && !on;
-    const uint32_t on_word = __ballot_sync(0xffffffffu, on), start_word = __ballot_sync(0xffffffffu, start);
-    if ((tid & 31) == 0) {
-        goes_on[tid >> 5] = on_word;
-        starts[tid >> 5] = start_word;
+    for (int i = tid; i < ((near + 31) & ~31); i += kThreads) {
+        const int v = i < near ? sl[i + 1] : -2;
+        const bool on = v > 0 && v == sl[i] + 1 && (v & mask) != 0;
+        const uint32_t on_word = __ballot_sync(0xffffffffu, on);
+        const uint32_t start_word = __ballot_sync(0xffffffffu, i < a.window && v >= 0 && !on);
+        if ((tid & 31) == 0) {
+            goes_on[i >> 5] = on_word;
+            starts[i >> 5] = start_word;
+        }
     }
     __syncthreads();
 
@@ -114,82 +196,73 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const StoreArgs a)
         for (uint32_t left = starts[word]; left; left &= left - 1) {
             const int i = word * 32 + __ffs(left) - 1;
             int n = 1;
-            while (i + n < kThreads && (goes_on[(i + n) >> 5] >> ((i + n) & 31) & 1u))
-                ++n;
-            const int slot = sl[i + 1], blk = slot / a.block, off = slot & mask;
+            for (int k = i + 1; k < near;) {
+                const uint32_t stop = ~goes_on[k >> 5] >> (k & 31);
+                const int ones = stop ? __ffs(stop) - 1 : 32 - (k & 31);
+                n += ones;
+                k += ones;
+                if (stop)
+                    break;
+            }
+            n = min(n, mask + 1);
+            const int slot = sl[i + 1], blk = slot >> a.shift, off = slot & mask;
             const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + h;
-            uint8_t* codes = a.codes[side] + unit * a.block * D;
+            uint8_t* codes = a.codes[side] + (unit << a.shift) * D;
             float* scale = a.scale[side] + unit;
 
             // ---- the rows, and the largest |x|
             uint4 v[kPieces];
-            uint32_t top = 0;
+            const uint16_t* src = x + (w0 + i + tid / kCols) * a.row_stride + (tid % kCols) * 8;
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const int p = tid + j * kThreads;
                 v[j] = make_uint4(0, 0, 0, 0);
-                if (p < n * kCols) {
-                    const int64_t row = w0 + i + p / kCols;
-                    v[j] = *reinterpret_cast<const uint4*>(x + row * a.row_stride + (p % kCols) * 8);
-                }
+                if (tid + j * kThreads < n * kCols)
+                    v[j] = __ldcs(reinterpret_cast<const uint4*>(src + j * (kThreads / kCols) * a.row_stride));
             }
             float was = off ? *scale : 0.0f;
+            uint32_t top = 0;                                      // 16-bit magnitudes order as integers
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                if (j * kThreads < n * kCols) {
-                    float f[8];
-                    widen<kF16>(v[j], f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
-                }
+                const uint32_t m = __vmaxu2(__vmaxu2(v[j].x & 0x7fff7fffu, v[j].y & 0x7fff7fffu),
+                                            __vmaxu2(v[j].z & 0x7fff7fffu, v[j].w & 0x7fff7fffu));
+                top = __vmaxu2(top, m);
             }
-            top = block_max(top, red);
-            if (top >= 0x7f800000u) {
-                // an infinity or a NaN: the maximum again over the finite values, NaN becomes 0
+            top = block_max<kThreads>(max(top & 0xffffu, top >> 16), red);
+            constexpr uint32_t kInf = kF16 ? 0x7c00u : 0x7f80u;
+            bool exact = false;
+            if (top >= kInf) {
+                // an infinity or a NaN: the maximum again over the finite values; NaN becomes 0
                 top = 0;
 #pragma unroll
                 for (int j = 0; j < kPieces; ++j) {
-                    float f[8];
-                    widen<kF16>(v[j], f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t b = __float_as_uint(f[e]) & 0x7fffffffu;
-                        top = max(top, b < 0x7f800000u ? b : 0u);
-                        if (b > 0x7f800000u) {
-                            uint32_t* w = e < 2 ? &v[j].x : e < 4 ? &v[j].y : e < 6 ? &v[j].z : &v[j].w;
-                            *w &= (e & 1) ? 0x0000ffffu : 0xffff0000u;
-                        }
-                    }
+                    clean(v[j].x, top, kInf);
+                    clean(v[j].y, top, kInf);
+                    clean(v[j].z, top, kInf);
+                    clean(v[j].w, top, kInf);
                 }
-                top = block_max(top, red);
+                top = block_max<kThreads>(top, red);
+                exact = true;
                 if (tid == 0)
                     report(a.err, RKV_ERR_INVALID_ARG);
             }
 
             // ---- the block's scale
-            if (!(was >= 0.0f && was <= FLT_MAX)) {
+            if (!(was == 0.0f || (was >= FLT_MIN && was <= FLT_MAX))) {
                 was = 0.0f;
                 if (tid == 0)
                     report(a.err, RKV_ERR_CORRUPT);
             }
-            const float amax = __uint_as_float(top);
+            const float amax = kF16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(top)))
+                                    : bf16_bits_to_f32(top);
             const float need = amax > 0.0f ? fmaxf(__fmul_rn(amax, 1.0f / qmax<kE4M3>()), kMinScale) : 0.0f;
-            float s = need;
-            int up = 0;
-            if (was > 0.0f) {
-                if (need > was) {
-                    int e_was, e_need;
-                    const float m_was = frexpf(was, &e_was), m_need = frexpf(need, &e_need);
-                    up = e_need - e_was + (m_need > m_was ? 1 : 0);
-                }
-                s = ldexpf(was, up);
-            }
+            const int up = was > 0.0f && need > was ? doublings(was, need) : 0;
+            float s = was > 0.0f ? was : need;
             if (up > 0) {
+                s = __uint_as_float(__float_as_uint(was) + (static_cast<uint32_t>(up) << 23));
                 // rows already in the block, at the larger scale
-                const float down = ldexpf(1.0f, -up);
+                const float down = pow2(-up);
                 for (int p = tid; p < off * (D / 16); p += kThreads) {
-                    uint4 c = reinterpret_cast<const uint4*>(codes)[p];
+                    const uint4 c = reinterpret_cast<const uint4*>(codes)[p];
                     uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -206,33 +279,41 @@ __global__ void __launch_bounds__(kThreads) kv8_store_kernel(const StoreArgs a)
                 *scale = s;
 
             // ---- the new codes
+            const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            exact |= s < kMinScale;
+            uint8_t* dst = codes + (off + tid / kCols) * D + (tid % kCols) * 8;
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
-                const int p = tid + j * kThreads;
-                if (p < n * kCols) {
+                if (tid + j * kThreads < n * kCols) {
                     float f[8];
                     widen<kF16>(v[j], f);
-                    uint32_t o[2] = {0, 0};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float t = s > 0.0f ? __fdiv_rn(f[e], s) : 0.0f;
-                        o[e >> 2] |= encode<kE4M3>(t) << (8 * (e & 3));
-                    }
-                    *reinterpret_cast<uint2*>(codes + (off + p / kCols) * D + (p % kCols) * 8) = make_uint2(o[0], o[1]);
+                    const uint2 o = s > 0.0f ? quantise8<kE4M3>(f, s, r, exact) : make_uint2(0, 0);
+                    *reinterpret_cast<uint2*>(dst + j * (kThreads / kCols) * D) = o;
                 }
             }
         }
     }
 }
 
+template <int D, int kThreads, bool kE4M3>
+cudaError_t launch_n(const StoreArgs& a, bool f16, dim3 grid, cudaStream_t st)
+{
+    if (f16)
+        kv8_store_kernel<D, kThreads, kE4M3, true><<<grid, kThreads, 0, st>>>(a);
+    else
+        kv8_store_kernel<D, kThreads, kE4M3, false><<<grid, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <int D, bool kE4M3>
 cudaError_t launch_t(const StoreArgs& a, bool f16, dim3 grid, cudaStream_t st)
 {
-    if (f16)
-        kv8_store_kernel<D, kE4M3, true><<<grid, kThreads, 0, st>>>(a);
-    else
-        kv8_store_kernel<D, kE4M3, false><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    switch ((D << a.shift) / 64) {
+    case 256: return launch_n<D, 256, kE4M3>(a, f16, grid, st);
+    case 128: return launch_n<D, 128, kE4M3>(a, f16, grid, st);
+    case 64: return launch_n<D, 64, kE4M3>(a, f16, grid, st);
+    default: return launch_n<D, 32, kE4M3>(a, f16, grid, st);
+    }
 }
 
 }  // namespace
@@ -242,7 +323,9 @@ cudaError_t launch_kv8_store(const rkv_kv8_cache& c, const void* K_new, const vo
 {
     StoreArgs a;
     a.Hkv = c.n_kv_heads;
-    a.block = c.block_size;
+    a.shift = 0;
+    while ((1 << a.shift) < c.block_size)
+        ++a.shift;
     a.n_blocks = c.n_blocks;
     // up to a few rows per request (a decode step): every row a window, so that no CTA does several
     // runs one after the other; otherwise about one run per window
