@@ -3,14 +3,36 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(c q_i.k_j - m_i),  c = scale log2(e),  j <= L - n + i
 //
 // One pass over the keys in tiles of 128 with the running maximum m_i and sum of each row.  The 128 rows of a
-// tile are tokens x query heads of one kv-head: row r = token r / G, head r % G, so the G heads that share K
-// and V share every tile of them, and short prompts fill the rows G times better than one head would.
-// S = Q K^T and O += P V are tcgen05 products (M 128, N 128, fp32 accumulators in TMEM); P goes back to TMEM in
-// the input type as the A operand of the second product.  That rounding (half a step of the input type per
-// weight, the sum l taken before it) is no larger than the one of a 16-bit output.
+// query tile are tokens x query heads of one kv-head: row r = token r / G, head r % G, so the G heads that
+// share K and V share every tile of them, and short prompts fill the rows G times better than one head would.
+// S = Q K^T and O += P V are tcgen05 products (M 128, N up to 128, fp32 accumulators in TMEM); P goes back to
+// TMEM, over S, in the input type as the A operand of the second product.  That rounding (half a step of the
+// input type per weight, the sum l taken before it) is no larger than the one of a 16-bit output.
+//
+// What bounds it: per 128 x 128 tile the two products take 1024 cycles of the tensor core at head_dim 128 (512 at
+// 64), and its 16384 exponentials 1024 cycles of the special-function unit.  So
+//   - a CTA works on two query tiles of the same kv-head in turn: while the softmax warps of one form P, the
+//     tensor core runs the other's products; K and V tiles serve both (one ring in shared memory, filled by TMA);
+//   - two threads share a row (TMEM lane), 64 keys each: a tile's softmax is on the critical path between its two
+//     products, and two warps per scheduler hide each other's latencies; they only exchange the row's maximum;
+//   - the accumulator is only rescaled when a row's maximum grew by more than 2^8: rare after the first
+//     tiles, and by the time S of a tile is there the previous product of the same rows is complete (one thread
+//     issues S after it), so the softmax warps do it themselves without a wait;
+//   - a share of the exponentials runs on the FMA pipes (exp2_pairs below);
+//   - each half hands its P over by itself, so the second product starts with the half that is ready.
+//
+// Work split: items (sequence, pair of query tiles, kv-head), sequences sorted by their number of keys and pairs
+// from the last (most keys) to the first, taken in snake order by one persistent CTA per SM.  Everything is
+// derived from the offsets on the device, so a captured graph follows them.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, then four groups of four: keys 0-63 and 64-127 of query tile 0, the same of
+// tile 1.  setmaxnreg moves registers from the first four warps to them.
+// Every wait is bounded (2 s); one that gives up records RKV_ERR_TIMEOUT, all roles leave their loops, and copies
+// and products in flight are waited for before TMEM is freed.
 #include <cudaTypedefs.h>
 
 #include <cfloat>
+#include <climits>
 #include <cmath>
 
 #include "device_common.cuh"
@@ -25,8 +47,8 @@ using namespace sm100;
 
 constexpr int kM = 128;                 // rows of a query tile (TMEM lanes)
 constexpr int kN = 128;                 // keys of a tile
-constexpr int kThreads = 128;
-constexpr uint32_t kTmemCols = 256;     // S (P over it): 128, O: 128
+constexpr int kThreads = 640;
+constexpr uint32_t kTmemCols = 512;     // S (P over it) of tiles 0, 1: 0, 128; O of tiles 0, 1: 256, 384
 constexpr float kNone = -1e30f;         // running maximum before any key
 constexpr float kLazy = 8.0f;           // the accumulator is rescaled when the maximum grows by 2^8
 
@@ -54,6 +76,67 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// ---- packed pairs of fp32 ---------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^x of a pair on the FMA pipes, x <= 2^6: x = n + f with n = rint(x) (taken from the low bits of x + 1.5 2^23),
+// 2^f by the degree-5 polynomial of least relative error on [-1/2, 1/2] (found by the Remez exchange; 7.5e-8, with
+// fp32 rounding under 2^-22), n added to the exponent field.  x is held at -125, where a weight no longer counts.
+__device__ __forceinline__ void exp2_pair(uint64_t x, float& r0, float& r1)
+{
+    float a, b;
+    unpair(x, a, b);
+    x = pair(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
+    const uint64_t magic = pair(12582912.0f, 12582912.0f), back = pair(-12582912.0f, -12582912.0f);
+    const uint64_t t = add2(x, magic);
+    const uint64_t f = fma2(add2(t, back), pair(-1.0f, -1.0f), x);
+    uint64_t p = pair(0.0013276471992533984f, 0.0013276471992533984f);
+    p = fma2(p, f, pair(0.009675541334453752f, 0.009675541334453752f));
+    p = fma2(p, f, pair(0.055507132734978495f, 0.055507132734978495f));
+    p = fma2(p, f, pair(0.24022119723839974f, 0.24022119723839974f));
+    p = fma2(p, f, pair(0.6931469670647609f, 0.6931469670647609f));
+    p = fma2(p, f, pair(1.0000000716546849f, 1.0000000716546849f));
+    float t0, t1;
+    unpair(t, t0, t1);
+    unpair(p, a, b);
+    r0 = __uint_as_float(__float_as_uint(a) + (__float_as_uint(t0) << 23));
+    r1 = __uint_as_float(__float_as_uint(b) + (__float_as_uint(t1) << 23));
+}
+
+// ---- tensor memory, TMA, descriptors -------------------------------------------------------
+
 // D[tmem] (+)= A[tmem] * B[smem]^T, kind::f16.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate)
@@ -66,36 +149,81 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+// 32 columns of this warp's TMEM lanes; the values may be used after tmem_arrived on them.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Orders the uses of v behind the volatile wait above.
+__device__ __forceinline__ void tmem_arrived(float* v)
+{
+    asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 4-D tiled TMA load (no multicast).
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar)
+// One lane of a converged warp, in a form that the compiler knows to be a single thread.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ void named_sync(int id, int n)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_regs()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int kRegs>
+__device__ __forceinline__ void fewer_regs()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// 4-D and 3-D tiled TMA loads (no multicast).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar)
 {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(smem_addr(dst)),
+        "[%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
 {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(smem_addr(dst)),
+        "[%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
 }
@@ -127,9 +255,11 @@ __device__ __forceinline__ uint32_t pack2(float x, float y)
     }
 }
 
+// ---- work items ------------------------------------------------------------------------------
+
 // Rows and keys of a sequence; ok = false if they leave q or K.
 struct Seq {
-    int q0, n, kv0, L, plane;
+    int q0, n, kv0, L;
     bool ok;
 };
 
@@ -142,12 +272,10 @@ __device__ __forceinline__ Seq sequence(const PrefillArgs& a, int b)
     if (a.kv_padded) {
         kv0 = a.kv_off ? a.kv_off[b] : 0;
         L = a.kv_len ? a.kv_len[b] : n;
-        s.plane = b;
     } else {
         const int32_t* off = a.kv_off ? a.kv_off : a.q_off;
         kv0 = off[b];
         L = a.kv_len ? a.kv_len[b] : static_cast<int64_t>(off[b + 1]) - kv0;
-        s.plane = 0;
     }
     s.ok = s.q0 >= 0 && n >= 0 && s.q0 + n <= a.q_rows && kv0 >= 0 && L >= 0 && kv0 + L <= a.kv_rows;
     s.n = s.ok ? static_cast<int>(n) : 0;
@@ -156,256 +284,510 @@ __device__ __forceinline__ Seq sequence(const PrefillArgs& a, int b)
     return s;
 }
 
+struct Schedule {
+    Seq seq[RKV_MAX_BATCH];
+    int key[RKV_MAX_BATCH];             // keys of sequence b, for the order
+    int order[RKV_MAX_BATCH];           // sequences by their keys, most first
+    int pairs[RKV_MAX_BATCH + 1];       // tile pairs before the i-th sequence of that order
+    int warp_tot[kThreads / 32];
+};
+
+// Sorts the sequences and counts their tile pairs (whole CTA).
+__device__ __forceinline__ void make_schedule(const PrefillArgs& a, Schedule& s)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Seq q = {};
+    if (tid < a.batch) {
+        q = sequence(a, tid);
+        s.seq[tid] = q;
+        s.key[tid] = q.L;
+        if (!q.ok && blockIdx.x == 0)
+            report(a.err, RKV_ERR_INVALID_ARG);
+    }
+    __syncthreads();
+    if (tid < a.batch) {
+        int rank = 0;
+        for (int b = 0; b < a.batch; ++b)
+            rank += s.key[b] > q.L || (s.key[b] == q.L && b < tid);
+        s.order[rank] = tid;
+    }
+    __syncthreads();
+    int v = tid < a.batch ? (s.seq[s.order[tid]].n + 2 * a.ntok - 1) / (2 * a.ntok) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, v, o);
+        v += lane >= o ? n : 0;
+    }
+    if (lane == 31)
+        s.warp_tot[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w)
+        v += s.warp_tot[w];
+    if (tid < a.batch)
+        s.pairs[tid + 1] = v;
+    if (tid == 0)
+        s.pairs[0] = 0;
+    __syncthreads();
+}
+
+// One item: query tiles of a pair start at tokens tok0 and tok0 + ntok; query tile t needs the key tiles 0 ..
+// nk(t) - 1 (none: the tile is empty or sees no key), of the last of which it sees the first last_width(t) keys, in
+// whole groups of 16 (the other tiles are seen whole by its last row).
+struct Item {
+    int q0, n, kv0, L, kvh, plane, tok0, ntok;
+    __device__ __forceinline__ int last_key(int t) const { return L - n + min(tok0 + (t + 1) * ntok, n) - 1; }
+    __device__ __forceinline__ int nk(int t) const
+    {
+        const int last = last_key(t);
+        return tok0 + t * ntok < n && last >= 0 ? last / kN + 1 : 0;
+    }
+    __device__ __forceinline__ int last_width(int t) const { return ((last_key(t) % kN) + 16) & ~15; }
+};
+
+// The r-th item of this CTA; false if there is none (with the snake order only the last round can lack one).
+__device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& sc, int r, Item& it)
+{
+    const unsigned P = gridDim.x, p = blockIdx.x;
+    const unsigned total = static_cast<unsigned>(sc.pairs[a.batch]) * a.Hkv;
+    const unsigned idx = r * P + ((r & 1) ? P - 1 - p : p);
+    if (idx >= total)
+        return false;
+    const int pr = static_cast<int>(idx / static_cast<unsigned>(a.Hkv));
+    it.kvh = static_cast<int>(idx) - pr * a.Hkv;
+    int lo = 0, hi = a.batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (sc.pairs[mid] <= pr)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int b = sc.order[lo];
+    const Seq q = sc.seq[b];
+    it.q0 = q.q0;
+    it.n = q.n;
+    it.kv0 = q.kv0;
+    it.L = q.L;
+    it.plane = a.kv_padded ? b : 0;
+    it.ntok = a.ntok;
+    it.tok0 = (sc.pairs[lo + 1] - 1 - pr) * 2 * a.ntok;
+    return true;
+}
+
 template <int D>
 struct Layout {
     static constexpr uint32_t tile = 128 * D * 2;
-    static constexpr uint32_t q = 0, k = tile, v = 2 * tile, bars = 3 * tile;
-    static constexpr uint32_t alloc = bars + 256 + 1024;
+    static constexpr int stages = D == 128 ? 4 : 8;           // K and V tiles in turn
+    static constexpr uint32_t q = 0, kv = 2 * tile, bars = kv + stages * tile;
+    static constexpr uint32_t alloc = bars + 512 + 1024;
 };
 
+template <int kStages>
 struct Bars {
-    uint64_t q_full, k_full, v_full, s_done, o_done, last;
+    uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages];
+    uint64_t s_full[2], p_ready[2][2], o_full[2], last;
     uint32_t tmem;
     int abort;
+    int issued;                 // ring slots filled so far (producer, at its end)
+    int q_issued[2];
 };
 
 template <int D, bool kF16>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                    const __grid_constant__ CUtensorMap mV, const PrefillArgs a)
 {
     using L = Layout<D>;
-    constexpr int kHalves = D / 64;
+    constexpr int kHalves = D / 64, kStages = L::stages;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    Bars* bars = reinterpret_cast<Bars*>(sm + L::bars);
-    __shared__ int s_seq, s_tile;
-    const int tid = threadIdx.x, warp = tid >> 5;
+    Bars<kStages>* bars = reinterpret_cast<Bars<kStages>*>(sm + L::bars);
+    static_assert(sizeof(Bars<kStages>) <= 512, "barrier block");
+    __shared__ Schedule sched;
+    __shared__ float s_max[2][2][2][kM], s_sum[2][2][2][kM];   // [query tile][parity][half]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &bars->abort;
 
-    // ---- the item: sequences in order, their tiles from the last (the longest) to the first
     if (tid == 0) {
-        int64_t left = blockIdx.x / a.Hkv;
-        int b = 0, tile = -1;
-        for (; b < a.batch; ++b) {
-            const Seq s = sequence(a, b);
-            if (!s.ok && blockIdx.x == 0)
-                report(a.err, RKV_ERR_INVALID_ARG);
-            const int nt = (s.n + a.ntok - 1) / a.ntok;
-            if (tile < 0) {
-                if (left < nt) {
-                    tile = nt - 1 - static_cast<int>(left);
-                    s_seq = b;
-                    if (blockIdx.x != 0)
-                        break;
-                }
-                left -= nt;
-            }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->q_full[t], 1);
+            mbar_init(&bars->q_empty[t], 1);
+            mbar_init(&bars->s_full[t], 1);
+            mbar_init(&bars->p_ready[t][0], 4);
+            mbar_init(&bars->p_ready[t][1], 4);
+            mbar_init(&bars->o_full[t], 1);
+            bars->q_issued[t] = 0;
         }
-        s_tile = tile;
-        mbar_init(&bars->q_full, 1);
-        mbar_init(&bars->k_full, 1);
-        mbar_init(&bars->v_full, 1);
-        mbar_init(&bars->s_done, 1);
-        mbar_init(&bars->o_done, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars->kv_full[i], 1);
+            mbar_init(&bars->kv_empty[i], 1);
+        }
         mbar_init(&bars->last, 1);
         bars->abort = 0;
+        bars->issued = 0;
         fence_mbar_init();
+        prefetch_tensormap(&mQ);
+        prefetch_tensormap(&mK);
+        prefetch_tensormap(&mV);
     }
-    __syncthreads();
-    if (s_tile < 0)
-        return;
-    if (warp == 0) {
+    if (warp == 1) {
         tmem_alloc(&bars->tmem, kTmemCols);
         tmem_relinquish();
     }
+    make_schedule(a, sched);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm_s = bars->tmem, tm_o = tm_s + 128;
-    const uint32_t lane_off = static_cast<uint32_t>(32 * warp) << 16;
-    volatile int* abort = &bars->abort;
+    const uint32_t tmem = bars->tmem;
+    const uint32_t q_smem = smem_addr(sm + L::q), kv_smem = smem_addr(sm + L::kv);
 
-    const Seq s = sequence(a, s_seq);
-    const int kvh = blockIdx.x % a.Hkv, tok0 = s_tile * a.ntok;
-    const int last_tok = min(tok0 + a.ntok, s.n) - 1;
-    const int64_t last_key = static_cast<int64_t>(s.L) - s.n + last_tok;
-    const int n_tiles = last_key >= 0 ? static_cast<int>(last_key / kN) + 1 : 0;
-    const int tok = tok0 + tid / a.G;
-    const int lim = s.L - s.n + tok;              // last key that this row sees
-    const uint32_t q_bytes = static_cast<uint32_t>(a.ntok * a.G * D * 2);
-    constexpr uint32_t idescS = idesc_f32<kF16>(kM, kN);
-    constexpr uint32_t idescO = idesc_f32<kF16>(kM, D) | (1u << 16);   // B (= V) MN-major
-
-    if (tid == 0 && n_tiles > 0) {
-        mbar_arrive_expect_tx(&bars->q_full, q_bytes);
-        for (int x = 0; x < kHalves; ++x)
-            tma_load_3d(sm + L::q + x * 16384, &mQ, 64 * x, kvh * a.G, s.q0 + tok0, &bars->q_full);
-    }
-    float m = kNone, l = 0.0f;
-    bool ok = true;
-    int issued = 0;
-    for (int j = 0; j < n_tiles; ++j) {
-        const uint32_t ph = j & 1;
-        const int k0 = j * kN;
-        if (tid == 0) {
-            // the previous product has read K, V, S and P
-            if (j > 0)
-                ok = ok && mbar_wait(&bars->o_done, ph ^ 1, abort);
-            if (ok) {
-                mbar_arrive_expect_tx(&bars->k_full, L::tile);
-                mbar_arrive_expect_tx(&bars->v_full, L::tile);
-                for (int x = 0; x < kHalves; ++x)
-                    tma_load_4d(sm + L::k + x * 16384, &mK, 64 * x, s.kv0 + k0, kvh, s.plane, &bars->k_full);
-                for (int x = 0; x < kHalves; ++x)
-                    tma_load_4d(sm + L::v + x * 16384, &mV, 64 * x, s.kv0 + k0, kvh, s.plane, &bars->v_full);
-                issued = j + 1;
-                if (j == 0)
-                    ok = mbar_wait(&bars->q_full, 0, abort);
-                ok = ok && mbar_wait(&bars->k_full, ph, abort);
-                if (ok) {
-                    tc_fence_after();
+    if (warp < 4) {
+        fewer_regs<64>();
+        Item it;
+        bool ok = true;
+        if (warp == 0 && lane == 0) {
+            // ---------------- TMA producer
+            const uint32_t q_bytes = static_cast<uint32_t>(a.ntok * a.G * D * 2);
+            uint32_t slot = 0, q_use0 = 0, q_use1 = 0;
+            auto load_q = [&](int t, uint32_t& use) {
+                if (use > 0)
+                    ok = ok && mbar_wait_sleep(&bars->q_empty[t], (use - 1) & 1, abort);
+                if (!ok)
+                    return;
+                mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
-                        mma_f16(tm_s, smem_desc_sw128(smem_addr(sm + L::q) + off),
-                                smem_desc_sw128(smem_addr(sm + L::k) + off), idescS, kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit(&bars->s_done);
+                for (int x = 0; x < kHalves; ++x)
+                    tma_load_3d(q_smem + t * L::tile + x * 16384, &mQ, 64 * x, it.kvh * a.G, it.q0 + it.tok0 + t * a.ntok,
+                                &bars->q_full[t]);
+                ++use;
+            };
+            auto load_kv = [&](const CUtensorMap* m, int j) {
+                const uint32_t st = slot % kStages, use = slot / kStages;
+                if (use > 0)
+                    ok = ok && mbar_wait_sleep(&bars->kv_empty[st], (use - 1) & 1, abort);
+                if (!ok)
+                    return;
+                mbar_arrive_expect_tx(&bars->kv_full[st], L::tile);
+#pragma unroll
+                for (int x = 0; x < kHalves; ++x)
+                    tma_load_4d(kv_smem + st * L::tile + x * 16384, m, 64 * x, it.kv0 + j * kN, it.kvh, it.plane,
+                                &bars->kv_full[st]);
+                ++slot;
+            };
+            for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
+                const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j == 0 && n0 > 0)
+                        load_q(0, q_use0);
+                    load_kv(&mK, j);
+                    if (j == 0 && n1 > 0)
+                        load_q(1, q_use1);
+                    load_kv(&mV, j);
                 }
             }
-            if (!ok)
+            if (!ok) {
+                if (!*abort)
+                    report(a.err, RKV_ERR_TIMEOUT);
                 *abort = 1;
-        }
-        ok = ok && mbar_wait(&bars->s_done, ph, abort);
-        if (!__syncthreads_and(ok))
-            break;
-        tc_fence_after();
-        float p[128];
+            }
+            bars->issued = static_cast<int>(slot);
+            bars->q_issued[0] = static_cast<int>(q_use0);
+            bars->q_issued[1] = static_cast<int>(q_use1);
+        } else if (warp == 1 && elect_one()) {
+            // ---------------- MMA issuer (one thread).  Per key tile j and query tile t: O_t += P_t V_j, then S_t = Q_t
+            // K_{j+1}, which overwrites P_t: the products of one thread complete in order.
+            constexpr uint32_t idescO = idesc_f32<kF16>(kM, D) | (1u << 16);   // B (= V) MN-major
+            const uint64_t q_desc = smem_desc_sw128(q_smem), k_desc = smem_desc_sw128(kv_smem),
+                           v_desc = smem_desc_mn(kv_smem);
+            constexpr uint32_t kTileDesc = L::tile >> 4;   // descriptors count 16 bytes
+            uint32_t slot = 0, q_ph = 0, p_ph = 0;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && mbar_wait(bar, parity, abort);
+                return ok;
+            };
+            // S_t over the 16-key groups that some row sees
+            auto issue_s = [&](int t, uint32_t st, int width) {
+                const uint32_t idesc = idesc_f32<kF16>(kM, 0) | (static_cast<uint32_t>(width >> 3) << 17);
+                const uint64_t qd = q_desc + t * kTileDesc, kd = k_desc + st * kTileDesc;
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            tmem_ld32(tm_s + 32 * x + lane_off, *reinterpret_cast<float(*)[32]>(&p[32 * x]));
-        const int cut = lim - k0;                  // columns past it are masked
-        float top = kNone;
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    constexpr uint32_t kHalfDesc = 16384 >> 4;
+                    const uint32_t off = (kk / 4) * kHalfDesc + (kk % 4) * 2;
+                    mma_f16(tmem + 128 * t, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&bars->s_full[t]);
+            };
+            for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
+                const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1);
+                if (n == 0)
+                    continue;
+                const int w0 = it.last_width(0), w1 = it.last_width(1);
+                if (!wait(&bars->kv_full[slot % kStages], (slot / kStages) & 1))
+                    break;
+                if (n0 > 0) {
+                    if (!wait(&bars->q_full[0], q_ph & 1))
+                        break;
+                    q_ph ^= 1;
+                    issue_s(0, slot % kStages, n0 == 1 ? w0 : kN);
+                    if (n0 == 1)
+                        mma_commit(&bars->q_empty[0]);
+                }
+                if (n1 > 0) {
+                    if (!wait(&bars->q_full[1], q_ph >> 1))
+                        break;
+                    q_ph ^= 2;
+                    issue_s(1, slot % kStages, n1 == 1 ? w1 : kN);
+                    if (n1 == 1)
+                        mma_commit(&bars->q_empty[1]);
+                }
+                mma_commit(&bars->kv_empty[slot % kStages]);
+                for (int j = 0; ok && j < n; ++j) {
+                    const uint32_t vs = (slot + 1) % kStages, ks = (slot + 2) % kStages;
+                    wait(&bars->kv_full[vs], ((slot + 1) / kStages) & 1);
+                    auto step = [&](int t, int nk, int last_width) {
+                        const uint32_t ph = (p_ph >> t) & 1;
+                        const int groups = j + 1 < nk ? kN / 16 : last_width / 16;
+                        const uint64_t vd = v_desc + vs * kTileDesc;
+                        if (!wait(&bars->p_ready[t][0], ph))
+                            return;
+                        tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < 128; ++x) {
-            p[x] = x <= cut ? p[x] * a.c : -INFINITY;
-            top = fmaxf(top, p[x]);
-        }
-        // the accumulator keeps its old maximum until the new one is 2^8 larger; a warp rescales together
-        float r = 1.0f;
-        if (j == 0 || top > m + kLazy) {
-            r = ex2(m - top);
-            m = fmaxf(m, top);
-            l *= r;
-        }
-        if (j > 0 && __any_sync(0xffffffffu, r != 1.0f)) {
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (kk < groups)
+                                mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + kk * (2048 >> 4), idescO,
+                                           (j > 0 || kk > 0) ? 1u : 0u);
+                        if (!wait(&bars->p_ready[t][1], ph))
+                            return;
+                        tc_fence_after();
 #pragma unroll
+                        for (int kk = 4; kk < 8; ++kk)
+                            if (kk < groups)
+                                mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + kk * (2048 >> 4), idescO,
+                                           1u);
+                        p_ph ^= 1u << t;
+                        if (j + 1 < nk) {
+                            if (!wait(&bars->kv_full[ks], ((slot + 2) / kStages) & 1))
+                                return;
+                            issue_s(t, ks, j + 2 < nk ? kN : last_width);
+                            if (j + 2 == nk)
+                                mma_commit(&bars->q_empty[t]);
+                        } else {
+                            mma_commit(&bars->o_full[t]);
+                        }
+                    };
+                    if (ok && j < n0)
+                        step(0, n0, w0);
+                    if (ok && j < n1)
+                        step(1, n1, w1);
+                    mma_commit(&bars->kv_empty[vs]);
+                    if (j + 1 < n)
+                        mma_commit(&bars->kv_empty[ks]);
+                    slot += 2;
+                }
+            }
+            if (!ok) {
+                if (!*abort)
+                    report(a.err, RKV_ERR_TIMEOUT);
+                *abort = 1;
+            }
+            // every product that this thread issued has completed before TMEM is released
+            volatile int never = 0;
+            mma_commit(&bars->last);
+            mbar_wait(&bars->last, 0, &never);
+        }
+    } else {
+        more_regs<104>();
+        // ---------------- softmax: two threads per row of query tile t (TMEM lane), half h of a key tile's columns each
+        const int t = (warp - 4) >> 3, h = ((warp - 4) >> 2) & 1, row = tid & 127;
+        const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tm_s = tmem + 128 * t + lane_off, tm_o = tmem + 256 + 128 * t + (D / 2) * h + lane_off;
+        uint32_t s_use = 0, o_use = 0, slot = 0;
+        bool ok = true;
+        Item it;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = ok && mbar_wait(bar, parity, abort);
+            ok = __all_sync(0xffffffffu, got);
+            tc_fence_after();
+        };
+        // after a wait gave up the loops go on without work, so that the named barriers stay matched
+        for (int r = 0; get_item(a, sched, r, it); ++r) {
+            const int nk = it.nk(t), n = max(nk, it.nk(1 - t));
+            const int lim = it.L - it.n + it.tok0 + t * a.ntok + row / a.G;   // last key that this row sees
+            // keys of the last tile, if rows of V behind them share their group of 16
+            const int tail = nk == n && (it.L & 15) && n * kN > it.L ? it.L - (n - 1) * kN : 0;
+            float m = kNone;
+            uint64_t sum = pair(0.0f, 0.0f);
+            for (int j = 0; j < nk; ++j) {
+                wait(&bars->s_full[t], s_use & 1);
+                ++s_use;
+                float s[64];
+                tmem_ld32_async(tm_s + 64 * h, s);
+                tmem_ld32_async(tm_s + 64 * h + 32, s + 32);
+                tmem_ld_wait();
+                tmem_arrived(s);
+                tmem_arrived(s + 32);
+                const int cut = lim - j * kN - 64 * h;      // columns past it are masked
+                if (__any_sync(0xffffffffu, cut < 63)) {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        s[x] = x <= cut ? s[x] : -INFINITY;
+                }
+                float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]), t2 = max3(s[6], s[7], s[8]),
+                      t3 = max3(s[9], s[10], s[11]);
+#pragma unroll
+                for (int x = 12; x + 8 <= 64; x += 8) {
+                    t0 = max3(t0, s[x], s[x + 1]);
+                    t1 = max3(t1, s[x + 2], s[x + 3]);
+                    t2 = max3(t2, s[x + 4], s[x + 5]);
+                    t3 = max3(t3, s[x + 6], s[x + 7]);
+                }
+                t0 = max3(t0, s[60], s[61]);
+                t1 = max3(t1, s[62], s[63]);
+                float top = fmaxf(max3(t0, t1, t2), t3);
+                // the other half's maximum; behind this barrier both have read S, so P may overwrite it
+                s_max[t][j & 1][h][row] = top;
+                named_sync(1 + t, 256);
+                top = fmaxf(top, s_max[t][j & 1][1 - h][row]) * a.c;
+                // the accumulator keeps its old maximum until the new one is 2^8 larger; a warp rescales together
+                float f = 1.0f;
+                if (j == 0 || top > m + kLazy) {
+                    f = ex2(m - top);
+                    m = fmaxf(m, top);
+                }
+                if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                    float x0, x1;
+                    unpair(sum, x0, x1);
+                    sum = pair(x0 * f, x1 * f);
+#pragma unroll 1
+                    for (int x = 0; x < D / 32; ++x) {
+                        uint32_t w[16];
+                        float o[16];
+                        tmem_ld16(tm_o + 16 * x, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = __float_as_uint(o[i] * f);
+                        tmem_st16(tm_o + 16 * x, w);
+                    }
+                }
+                if (tail > 0 && j == nk - 1) {
+                    // V rows behind the last key, within its group of 16, meet weights of 0 in the product: they may
+                    // hold NaN and are zeroed, by the warps of each query tile before they hand over P
+                    const uint32_t vs = slot + 2 * j + 1;
+                    wait(&bars->kv_full[vs % kStages], (vs / kStages) & 1);
+                    for (int i = 128 * h + row; ok && i < (16 - (tail & 15)) * kHalves * 8; i += 256) {
+                        const int key = tail + i / (kHalves * 8), x = (i >> 3) % kHalves;
+                        *reinterpret_cast<uint4*>(sm + L::kv + (vs % kStages) * L::tile + x * 16384 + key * 128 +
+                                                  (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    named_sync(1 + t, 256);
+                }
+                const uint64_t cc = pair(a.c, a.c), off = pair(kBias<kF16> - m, kBias<kF16> - m);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float& u = s[16 * x + 2 * i];
+                        float& v = s[16 * x + 2 * i + 1];
+                        const uint64_t e = fma2(pair(u, v), cc, off);
+                        if (i % 4 == 3) {
+                            exp2_pair(e, u, v);
+                        } else {
+                            float e0, e1;
+                            unpair(e, e0, e1);
+                            u = ex2(e0);
+                            v = ex2(e1);
+                        }
+                        w[i] = pack2<kF16>(u, v);
+                    }
+                    tmem_st8(tm_s + 32 * h + 8 * x, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars->p_ready[t][h]);
+                // the sum, off the way of the second product
+                uint64_t a0 = pair(s[0], s[1]), a1 = pair(s[2], s[3]);
+#pragma unroll
+                for (int x = 4; x < 64; x += 4) {
+                    a0 = add2(a0, pair(s[x], s[x + 1]));
+                    a1 = add2(a1, pair(s[x + 2], s[x + 3]));
+                }
+                sum = add2(sum, add2(a0, a1));
+            }
+            if (nk > 0) {
+                wait(&bars->o_full[t], o_use & 1);
+                ++o_use;
+            }
+            slot += 2 * n;
+            // the row's sum from both halves
+            float l0, l1;
+            unpair(sum, l0, l1);
+            float l = l0 + l1;
+            s_sum[t][r & 1][h][row] = l;
+            named_sync(1 + t, 256);
+            l += s_sum[t][r & 1][1 - h][row];
+            get_item(a, sched, r, it);                      // not kept in registers over the loop
+            const int row_tok = row / a.G, tok = it.tok0 + t * a.ntok + row_tok;
+            const bool store = ok && row < a.ntok * a.G && tok < it.n, sees = lim >= 0;
+            const int head = it.kvh * a.G + row - row_tok * a.G;
+            const int64_t q_row = static_cast<int64_t>(it.q0) + tok;
+            const float inv = sees ? 1.0f / l : 0.0f;
+            if (store && a.lse && h == 0)
+                a.lse[q_row * a.Hq + head] = sees ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            const int64_t e = q_row * a.out_row_stride + head * a.out_head_stride + (D / 2) * h;
+            // 16 columns at a time: few registers, and O of 0 keys (nothing was written there) times 0 is not formed
+#pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
-                float o[32];
-                uint32_t w[32];
-                tmem_ld32(tm_o + 32 * x + lane_off, o);
+                float o[16];
+                tmem_ld16(tm_o + 16 * x, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    w[i] = __float_as_uint(o[i] * r);
-                tmem_st32(tm_o + 32 * x + lane_off, w);
+                for (int i = 0; i < 16; ++i)
+                    o[i] = sees ? o[i] * inv : 0.0f;
+                if (store) {
+                    if (a.out_dtype == RKV_DTYPE_F32) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + e + 16 * x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + e + 16 * x);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            dst[i] = make_uint4(pack2<kF16>(o[8 * i], o[8 * i + 1]), pack2<kF16>(o[8 * i + 2], o[8 * i + 3]),
+                                                pack2<kF16>(o[8 * i + 4], o[8 * i + 5]),
+                                                pack2<kF16>(o[8 * i + 6], o[8 * i + 7]));
+                    }
+                }
             }
+            // the next item's first product overwrites O: it is ordered behind these loads by p_ready
+            tc_fence_before();
         }
-        float sum = 0.0f;
-#pragma unroll
-        for (int x = 0; x < 128; ++x) {
-            p[x] = ex2(p[x] - (m - kBias<kF16>));
-            sum += p[x];
-        }
-        l += sum;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                w[i] = pack2<kF16>(p[64 * x + 2 * i], p[64 * x + 2 * i + 1]);
-            tmem_st32(tm_s + 32 * x + lane_off, w);
-        }
-        tmem_st_wait();
-        if (k0 + kN > s.L) {
-            // rows of V behind the sequence's keys meet weights of 0: zero them, they may hold NaN
-            ok = ok && mbar_wait(&bars->v_full, ph, abort);
-            if (ok && tid >= s.L - k0) {
-                for (int x = 0; x < kHalves; ++x)
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4*>(sm + L::v + x * 16384 + tid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-        }
-        tc_fence_before();
-        if (!__syncthreads_and(ok))
-            break;
-        if (tid == 0) {
-            ok = mbar_wait(&bars->v_full, ph, abort);
-            if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < kN / 16; ++kk)
-                    mma_f16_ts(tm_o, tm_s + 8 * kk, smem_desc_mn(smem_addr(sm + L::v) + kk * 2048), idescO,
-                               (j > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(&bars->o_done);
-            } else {
-                *abort = 1;
-            }
+        if (!ok && lane == 0) {
+            if (!*abort)
+                report(a.err, RKV_ERR_TIMEOUT);
+            *abort = 1;
         }
     }
-    if (n_tiles > 0) {
-        ok = ok && mbar_wait(&bars->o_done, (n_tiles - 1) & 1, abort);
-        ok = __syncthreads_and(ok);
-        tc_fence_after();
-    }
-    if (ok) {
-        const bool store = tid < a.ntok * a.G && tok < s.n;
-        const int head = kvh * a.G + tid % a.G;
-        const int64_t row = s.q0 + tok;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        if (store && a.lse)
-            a.lse[row * a.Hq + head] = l > 0.0f ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        const int64_t e = row * a.out_row_stride + head * a.out_head_stride;
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-            float o[32];
-            if (n_tiles > 0)
-                tmem_ld32(tm_o + 32 * x + lane_off, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                o[i] = l > 0.0f ? o[i] * inv : 0.0f;
-            if (!store)
-                continue;
-            if (a.out_dtype == RKV_DTYPE_F32) {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + e + 32 * x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            } else {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + e + 32 * x);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dst[i] = make_uint4(pack2<kF16>(o[8 * i], o[8 * i + 1]), pack2<kF16>(o[8 * i + 2], o[8 * i + 3]),
-                                        pack2<kF16>(o[8 * i + 4], o[8 * i + 5]), pack2<kF16>(o[8 * i + 6], o[8 * i + 7]));
-            }
-        }
-    } else if (tid == 0) {
-        report(a.err, RKV_ERR_TIMEOUT);
-        // copies and products in flight end (waited for with the same limit) before the CTA does
+
+    // copies that are still in flight (only after an abort) land before the CTA may exit
+    __syncthreads();
+    if (tid == 0) {
         volatile int never = 0;
-        mbar_wait(&bars->q_full, 0, &never);
-        if (issued > 0) {
-            mbar_wait(&bars->k_full, (issued - 1) & 1, &never);
-            mbar_wait(&bars->v_full, (issued - 1) & 1, &never);
-        }
-        mma_commit(&bars->last);
-        mbar_wait(&bars->last, 0, &never);
+        const int n = bars->issued;
+        for (int i = n > kStages ? n - kStages : 0; i < n; ++i)
+            mbar_wait(&bars->kv_full[i % kStages], (i / kStages) & 1, &never);
+        for (int t = 0; t < 2; ++t)
+            if (bars->q_issued[t] > 0)
+                mbar_wait(&bars->q_full[t], (bars->q_issued[t] - 1) & 1, &never);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tm_s, kTmemCols);
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -437,13 +819,13 @@ bool make_map(CUtensorMap* m, const void* base, bool f16, int rank, const cuuint
 
 template <int D, bool kF16>
 cudaError_t launch_t(const CUtensorMap& mQ, const CUtensorMap& mK, const CUtensorMap& mV, const PrefillArgs& a,
-                     int64_t items, cudaStream_t st)
+                     int ctas, cudaStream_t st)
 {
     auto kern = prefill_kernel<D, kF16>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::alloc);
     if (e != cudaSuccess)
         return e;
-    kern<<<static_cast<unsigned>(items), kThreads, Layout<D>::alloc, st>>>(mQ, mK, mV, a);
+    kern<<<ctas, kThreads, Layout<D>::alloc, st>>>(mQ, mK, mV, a);
     return cudaGetLastError();
 }
 
@@ -453,7 +835,6 @@ cudaError_t launch_prefill(const rkv_prefill_config& c, const void* q, const voi
                            const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_len, void* out, float* lse,
                            int32_t* err, int sms, cudaStream_t st)
 {
-    (void)sms;
     if (!map_encoder())
         return cudaErrorNotSupported;
     PrefillArgs a;
@@ -493,11 +874,14 @@ cudaError_t launch_prefill(const rkv_prefill_config& c, const void* q, const voi
     if (!make_map(&mQ, q, f16, 3, qd, qs, qb) || !make_map(&mK, K, f16, 4, kd, ks, kb) ||
         !make_map(&mV, V, f16, 4, kd, ks, kb))
         return cudaErrorInvalidValue;
-    // the tiles are known on the device only: at most one partial tile per sequence
-    const int64_t items = (c.q_rows / a.ntok + c.batch) * c.n_kv_heads;
+    // the items are known on the device only: at most one partial pair of tiles per sequence
+    const int64_t items = (c.q_rows / (2 * a.ntok) + c.batch) * c.n_kv_heads;
+    if (items > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const int ctas = static_cast<int>(items < sms ? items : sms);
     if (c.head_dim == 128)
-        return f16 ? launch_t<128, true>(mQ, mK, mV, a, items, st) : launch_t<128, false>(mQ, mK, mV, a, items, st);
-    return f16 ? launch_t<64, true>(mQ, mK, mV, a, items, st) : launch_t<64, false>(mQ, mK, mV, a, items, st);
+        return f16 ? launch_t<128, true>(mQ, mK, mV, a, ctas, st) : launch_t<128, false>(mQ, mK, mV, a, ctas, st);
+    return f16 ? launch_t<64, true>(mQ, mK, mV, a, ctas, st) : launch_t<64, false>(mQ, mK, mV, a, ctas, st);
 }
 
 }  // namespace rkv
