@@ -2,31 +2,31 @@
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(c q_i.k_j - m_i),  c = scale log2(e),  j <= L - n + i
 //
-// One pass over the keys in tiles of 128 with the running maximum m_i and sum of each row.  The 128 rows of a
-// query tile are tokens x query heads of one kv-head: row r = token r / G, head r % G, so the G heads that
-// share K and V share every tile of them, and short prompts fill the rows G times better than one head would.
+// One pass over the keys in tiles of 64 with the running maximum m_i and sum of each row.  The 128 rows of a query
+// tile are tokens x query heads of one kv-head: row r = token r / G, head r % G, so the G heads that share K and V
+// share every tile of them, and short prompts fill the rows G times better than one head would.
 // S = Q K^T and O += P V are tcgen05 products (M 128, N up to 128, fp32 accumulators in TMEM); P goes back to
 // TMEM, over S, in the input type as the A operand of the second product.  That rounding (half a step of the
 // input type per weight, the sum l taken before it) is no larger than the one of a 16-bit output.
 //
-// What bounds it: per 128 x 128 tile the two products take 1024 cycles of the tensor core at head_dim 128 (512 at
-// 64), and its 16384 exponentials 1024 cycles of the special-function unit.  So
-//   - a CTA works on two query tiles of the same kv-head in turn: while the softmax warps of one form P, the
-//     tensor core runs the other's products; K and V tiles serve both (one ring in shared memory, filled by TMA);
-//   - two threads share a row (TMEM lane), 64 keys each: a tile's softmax is on the critical path between its two
-//     products, and two warps per scheduler hide each other's latencies; they only exchange the row's maximum;
-//   - the accumulator is only rescaled when a row's maximum grew by more than 2^8: rare after the first
-//     tiles, and by the time S of a tile is there the previous product of the same rows is complete (one thread
-//     issues S after it), so the softmax warps do it themselves without a wait;
-//   - a share of the exponentials runs on the FMA pipes (exp2_pairs below);
-//   - each half hands its P over by itself, so the second product starts with the half that is ready.
+// What bounds it: per 128 x 64 tile the two products take 640 cycles of the tensor core at head_dim 128 (S 384: with
+// N 64 the reads of Q from shared memory set its pace; P V 256), the 8192 exponentials 512 cycles of the
+// special-function unit, and S -> softmax -> P V is one chain of dependent steps with several hundred cycles of
+// signalling in it.  So
+//   - a CTA works on two query tiles of the same kv-head, each with its own MMA issuer and softmax warps, and K and
+//     V tiles serve both (one ring in shared memory, filled by TMA);
+//   - each query tile has two S buffers in TMEM (that is what tiles of 64 keys buy: O of two tiles and four S
+//     buffers fill the 512 columns), so the next S is formed while this one's softmax is at work;
+//   - one thread owns one row (TMEM lane): no shuffles, and the row's maximum and sum never leave registers;
+//   - the accumulator is only rescaled when a row's maximum grew by more than 2^8: rare after the first tiles, so
+//     almost no step waits for the product before it;
+//   - a share of the exponentials runs on the FMA pipes (exp2_pair below).
 //
 // Work split: items (sequence, pair of query tiles, kv-head), sequences sorted by their number of keys and pairs
 // from the last (most keys) to the first, taken in snake order by one persistent CTA per SM.  Everything is
 // derived from the offsets on the device, so a captured graph follows them.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, then four groups of four: keys 0-63 and 64-127 of query tile 0, the same of
-// tile 1.  setmaxnreg moves registers from the first four warps to them.
+// Warps: 0 TMA producer, 1 and 2 MMA issuers of query tiles 0 and 1, 4-7 and 8-11 their softmax.
 // Every wait is bounded (2 s); one that gives up records RKV_ERR_TIMEOUT, all roles leave their loops, and copies
 // and products in flight are waited for before TMEM is freed.
 #include <cudaTypedefs.h>
@@ -46,10 +46,11 @@ namespace {
 using namespace sm100;
 
 constexpr int kM = 128;                 // rows of a query tile (TMEM lanes)
-constexpr int kN = 128;                 // keys of a tile
-constexpr int kThreads = 640;
-constexpr uint32_t kTmemCols = 512;     // S (P over it) of tiles 0, 1: 0, 128; O of tiles 0, 1: 256, 384
+constexpr int kN = 64;                  // keys of a tile
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;     // S (P over it) of query tile t, two buffers: 128 t, 128 t + 64; O: 256 + 128 t
 constexpr float kNone = -1e30f;         // running maximum before any key
+constexpr int kPoly = 4;                // every kPoly-th pair of exponentials goes to the FMA pipes (0: none)
 constexpr float kLazy = 8.0f;           // the accumulator is rescaled when the maximum grows by 2^8
 
 // Weights are kept times 2^kBias: binary16 then holds them up to 2^(8 + 7) and down to 2^-32 of the largest
@@ -175,13 +176,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // One lane of a converged warp, in a form that the compiler knows to be a single thread.
@@ -190,23 +184,6 @@ __device__ __forceinline__ bool elect_one()
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
-}
-
-__device__ __forceinline__ void named_sync(int id, int n)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-
-template <int kRegs>
-__device__ __forceinline__ void more_regs()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-template <int kRegs>
-__device__ __forceinline__ void fewer_regs()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // 4-D and 3-D tiled TMA loads (no multicast).
@@ -228,10 +205,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// MN-major operand in the 128-byte swizzle: 64-element blocks 16 KB apart, 8-key groups 1 KB apart.
+// MN-major operand in the 128-byte swizzle: 64-element blocks of kN rows, 8-key groups 1 KB apart.
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t start)
 {
-    return static_cast<uint64_t>((start >> 4) & 0x3fff) | (static_cast<uint64_t>(16384 >> 4) << 16) |
+    return static_cast<uint64_t>((start >> 4) & 0x3fff) | (static_cast<uint64_t>((kN * 128) >> 4) << 16) |
            (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
            (static_cast<uint64_t>(2) << 61);
 }
@@ -376,16 +353,16 @@ __device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& s
 
 template <int D>
 struct Layout {
-    static constexpr uint32_t tile = 128 * D * 2;
-    static constexpr int stages = D == 128 ? 4 : 8;           // K and V tiles in turn
-    static constexpr uint32_t q = 0, kv = 2 * tile, bars = kv + stages * tile;
+    static constexpr uint32_t qtile = kM * D * 2, tile = kN * D * 2;
+    static constexpr int stages = 8;                          // K and V tiles in turn
+    static constexpr uint32_t q = 0, kv = 2 * qtile, bars = kv + stages * tile;
     static constexpr uint32_t alloc = bars + 512 + 1024;
 };
 
 template <int kStages>
 struct Bars {
     uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages];
-    uint64_t s_full[2], p_ready[2][2], o_full[2], last;
+    uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], last[2];   // [query tile][buffer]
     uint32_t tmem;
     int abort;
     int issued;                 // ring slots filled so far (producer, at its end)
@@ -404,7 +381,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars<kStages>* bars = reinterpret_cast<Bars<kStages>*>(sm + L::bars);
     static_assert(sizeof(Bars<kStages>) <= 512, "barrier block");
     __shared__ Schedule sched;
-    __shared__ float s_max[2][2][2][kM], s_sum[2][2][2][kM];   // [query tile][parity][half]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &bars->abort;
 
@@ -412,17 +388,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->q_full[t], 1);
             mbar_init(&bars->q_empty[t], 1);
-            mbar_init(&bars->s_full[t], 1);
-            mbar_init(&bars->p_ready[t][0], 4);
-            mbar_init(&bars->p_ready[t][1], 4);
-            mbar_init(&bars->o_full[t], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&bars->s_full[t][b], 1);
+                mbar_init(&bars->p_ready[t][b], 4);
+                mbar_init(&bars->pv_done[t][b], 1);
+            }
             bars->q_issued[t] = 0;
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars->kv_full[i], 1);
-            mbar_init(&bars->kv_empty[i], 1);
+            mbar_init(&bars->kv_empty[i], 2);
         }
-        mbar_init(&bars->last, 1);
+        mbar_init(&bars->last[0], 1);
+        mbar_init(&bars->last[1], 1);
         bars->abort = 0;
         bars->issued = 0;
         fence_mbar_init();
@@ -442,7 +420,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_smem = smem_addr(sm + L::q), kv_smem = smem_addr(sm + L::kv);
 
     if (warp < 4) {
-        fewer_regs<64>();
         Item it;
         bool ok = true;
         if (warp == 0 && lane == 0) {
@@ -457,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(&bars->q_full[t], q_bytes);
 #pragma unroll
                 for (int x = 0; x < kHalves; ++x)
-                    tma_load_3d(q_smem + t * L::tile + x * 16384, &mQ, 64 * x, it.kvh * a.G, it.q0 + it.tok0 + t * a.ntok,
+                    tma_load_3d(q_smem + t * L::qtile + x * (kM * 128), &mQ, 64 * x, it.kvh * a.G, it.q0 + it.tok0 + t * a.ntok,
                                 &bars->q_full[t]);
                 ++use;
             };
@@ -470,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(&bars->kv_full[st], L::tile);
 #pragma unroll
                 for (int x = 0; x < kHalves; ++x)
-                    tma_load_4d(kv_smem + st * L::tile + x * 16384, m, 64 * x, it.kv0 + j * kN, it.kvh, it.plane,
+                    tma_load_4d(kv_smem + st * L::tile + x * (kN * 128), m, 64 * x, it.kv0 + j * kN, it.kvh, it.plane,
                                 &bars->kv_full[st]);
                 ++slot;
             };
@@ -493,97 +470,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             bars->issued = static_cast<int>(slot);
             bars->q_issued[0] = static_cast<int>(q_use0);
             bars->q_issued[1] = static_cast<int>(q_use1);
-        } else if (warp == 1 && elect_one()) {
-            // ---------------- MMA issuer (one thread).  Per key tile j and query tile t: O_t += P_t V_j, then S_t = Q_t
-            // K_{j+1}, which overwrites P_t: the products of one thread complete in order.
+        } else if ((warp == 1 || warp == 2) && elect_one()) {
+            // ---------------- MMA issuers: one thread per query tile t.  Step c (counted over all items) uses buffer c & 1 for S
+            // and, over it, P.  S of step c + 1 is formed before P of step c is waited for; it overwrites P of step c - 1,
+            // so it waits for that product (products into different accumulators are not ordered by their issue).
             constexpr uint32_t idescO = idesc_f32<kF16>(kM, D) | (1u << 16);   // B (= V) MN-major
-            const uint64_t q_desc = smem_desc_sw128(q_smem), k_desc = smem_desc_sw128(kv_smem),
-                           v_desc = smem_desc_mn(kv_smem);
             constexpr uint32_t kTileDesc = L::tile >> 4;   // descriptors count 16 bytes
-            uint32_t slot = 0, q_ph = 0, p_ph = 0;
+            const int t = warp - 1;
+            const uint64_t q_desc = smem_desc_sw128(q_smem + t * L::qtile), k_desc = smem_desc_sw128(kv_smem),
+                           v_desc = smem_desc_mn(kv_smem);
+            const uint32_t tm_s = tmem + 128 * t, tm_o = tmem + 256 + 128 * t;
+            uint32_t slot = 0, q_use = 0, c = 0;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = ok && mbar_wait(bar, parity, abort);
                 return ok;
             };
-            // S_t over the 16-key groups that some row sees
-            auto issue_s = [&](int t, uint32_t st, int width) {
-                const uint32_t idesc = idesc_f32<kF16>(kM, 0) | (static_cast<uint32_t>(width >> 3) << 17);
-                const uint64_t qd = q_desc + t * kTileDesc, kd = k_desc + st * kTileDesc;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    constexpr uint32_t kHalfDesc = 16384 >> 4;
-                    const uint32_t off = (kk / 4) * kHalfDesc + (kk % 4) * 2;
-                    mma_f16(tmem + 128 * t, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
-                }
-                mma_commit(&bars->s_full[t]);
-            };
             for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
-                const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1);
-                if (n == 0)
-                    continue;
-                const int w0 = it.last_width(0), w1 = it.last_width(1);
-                if (!wait(&bars->kv_full[slot % kStages], (slot / kStages) & 1))
-                    break;
-                if (n0 > 0) {
-                    if (!wait(&bars->q_full[0], q_ph & 1))
-                        break;
-                    q_ph ^= 1;
-                    issue_s(0, slot % kStages, n0 == 1 ? w0 : kN);
-                    if (n0 == 1)
-                        mma_commit(&bars->q_empty[0]);
-                }
-                if (n1 > 0) {
-                    if (!wait(&bars->q_full[1], q_ph >> 1))
-                        break;
-                    q_ph ^= 2;
-                    issue_s(1, slot % kStages, n1 == 1 ? w1 : kN);
-                    if (n1 == 1)
-                        mma_commit(&bars->q_empty[1]);
-                }
-                mma_commit(&bars->kv_empty[slot % kStages]);
-                for (int j = 0; ok && j < n; ++j) {
-                    const uint32_t vs = (slot + 1) % kStages, ks = (slot + 2) % kStages;
-                    wait(&bars->kv_full[vs], ((slot + 1) / kStages) & 1);
-                    auto step = [&](int t, int nk, int last_width) {
-                        const uint32_t ph = (p_ph >> t) & 1;
-                        const int groups = j + 1 < nk ? kN / 16 : last_width / 16;
-                        const uint64_t vd = v_desc + vs * kTileDesc;
-                        if (!wait(&bars->p_ready[t][0], ph))
-                            return;
-                        tc_fence_after();
+                const int nk = it.nk(t), n = max(nk, it.nk(1 - t)), last_width = it.last_width(t);
+                // K_j is ring slot `slot` + 2 j, V_j the next
+                for (int j = 0; ok && j <= n; ++j) {
+                    if (j < n) {
+                        const uint32_t ks = (slot + 2 * j) % kStages;
+                        if (!wait(&bars->kv_full[ks], ((slot + 2 * j) / kStages) & 1))
+                            break;
+                        if (j < nk) {
+                            // S over the 16-key groups that some row sees.  The first S of an item waits for every
+                            // product of the item before, the others for the one two steps earlier
+                            const uint32_t back = j == 0 ? 1 : 2, cs = c + j;
+                            if (j == 0 && !wait(&bars->q_full[t], q_use++ & 1))
+                                break;
+                            if (cs >= back && !wait(&bars->pv_done[t][(cs - back) & 1], ((cs - back) >> 1) & 1))
+                                break;
+                            const uint32_t width = j + 1 < nk ? kN : last_width;
+                            const uint32_t idesc = idesc_f32<kF16>(kM, 0) | ((width >> 3) << 17);
+                            const uint64_t kd = k_desc + ks * kTileDesc;
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            if (kk < groups)
-                                mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + kk * (2048 >> 4), idescO,
-                                           (j > 0 || kk > 0) ? 1u : 0u);
-                        if (!wait(&bars->p_ready[t][1], ph))
-                            return;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 4; kk < 8; ++kk)
-                            if (kk < groups)
-                                mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, vd + kk * (2048 >> 4), idescO,
-                                           1u);
-                        p_ph ^= 1u << t;
-                        if (j + 1 < nk) {
-                            if (!wait(&bars->kv_full[ks], ((slot + 2) / kStages) & 1))
-                                return;
-                            issue_s(t, ks, j + 2 < nk ? kN : last_width);
-                            if (j + 2 == nk)
+                            for (int kk = 0; kk < D / 16; ++kk)
+                                mma_f16(tm_s + 64 * (cs & 1), q_desc + (kk / 4) * ((kM * 128) >> 4) + (kk % 4) * 2,
+                                        kd + (kk / 4) * ((kN * 128) >> 4) + (kk % 4) * 2, idesc, kk > 0 ? 1u : 0u);
+                            mma_commit(&bars->s_full[t][cs & 1]);
+                            mma_commit(&bars->kv_empty[ks]);
+                            if (j + 1 == nk)
                                 mma_commit(&bars->q_empty[t]);
                         } else {
-                            mma_commit(&bars->o_full[t]);
+                            mbar_arrive(&bars->kv_empty[ks]);      // the other query tile's alone
                         }
-                    };
-                    if (ok && j < n0)
-                        step(0, n0, w0);
-                    if (ok && j < n1)
-                        step(1, n1, w1);
-                    mma_commit(&bars->kv_empty[vs]);
-                    if (j + 1 < n)
-                        mma_commit(&bars->kv_empty[ks]);
-                    slot += 2;
+                    }
+                    if (j > 0) {
+                        const uint32_t vslot = slot + 2 * j - 1, vs = vslot % kStages, cp = c + j - 1;   // V_{j - 1}
+                        if (!wait(&bars->kv_full[vs], (vslot / kStages) & 1))
+                            break;
+                        if (j - 1 < nk) {
+                            if (!wait(&bars->p_ready[t][cp & 1], (cp >> 1) & 1))
+                                break;
+                            tc_fence_after();
+                            const int groups = (j < nk ? kN : last_width) / 16;
+                            const uint64_t vd = v_desc + vs * kTileDesc;
+#pragma unroll
+                            for (int kk = 0; kk < kN / 16; ++kk)
+                                if (kk < groups)
+                                    mma_f16_ts(tm_o, tm_s + 64 * (cp & 1) + 8 * kk, vd + kk * (2048 >> 4), idescO,
+                                               (j > 1 || kk > 0) ? 1u : 0u);
+                            mma_commit(&bars->pv_done[t][cp & 1]);
+                            mma_commit(&bars->kv_empty[vs]);
+                        } else {
+                            mbar_arrive(&bars->kv_empty[vs]);
+                        }
+                    }
                 }
+                slot += 2 * n;
+                c += nk;
             }
             if (!ok) {
                 if (!*abort)
@@ -592,16 +548,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every product that this thread issued has completed before TMEM is released
             volatile int never = 0;
-            mma_commit(&bars->last);
-            mbar_wait(&bars->last, 0, &never);
+            mma_commit(&bars->last[t]);
+            mbar_wait(&bars->last[t], 0, &never);
         }
     } else {
-        more_regs<104>();
-        // ---------------- softmax: two threads per row of query tile t (TMEM lane), half h of a key tile's columns each
-        const int t = (warp - 4) >> 3, h = ((warp - 4) >> 2) & 1, row = tid & 127;
+        // ---------------- softmax: thread = row of query tile t = TMEM lane
+        const int t = (warp - 4) >> 2, row = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t tm_s = tmem + 128 * t + lane_off, tm_o = tmem + 256 + 128 * t + (D / 2) * h + lane_off;
-        uint32_t s_use = 0, o_use = 0, slot = 0;
+        const uint32_t tm_s = tmem + 128 * t + lane_off, tm_o = tmem + 256 + 128 * t + lane_off;
+        const int row_tok = row / a.G, row_head = row - row_tok * a.G;
+        uint32_t c = 0, slot = 0;                           // steps of this query tile, ring slots
         bool ok = true;
         Item it;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -609,25 +565,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, got);
             tc_fence_after();
         };
-        // after a wait gave up the loops go on without work, so that the named barriers stay matched
-        for (int r = 0; get_item(a, sched, r, it); ++r) {
-            const int nk = it.nk(t), n = max(nk, it.nk(1 - t));
-            const int lim = it.L - it.n + it.tok0 + t * a.ntok + row / a.G;   // last key that this row sees
-            // keys of the last tile, if rows of V behind them share their group of 16
-            const int tail = nk == n && (it.L & 15) && n * kN > it.L ? it.L - (n - 1) * kN : 0;
+        for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
+            const int nk = it.nk(t), tok = it.tok0 + t * a.ntok + row_tok;
+            const int lim = it.L - it.n + tok;              // last key that this row sees
+            const int n = max(nk, it.nk(1 - t));
             float m = kNone;
             uint64_t sum = pair(0.0f, 0.0f);
-            for (int j = 0; j < nk; ++j) {
-                wait(&bars->s_full[t], s_use & 1);
-                ++s_use;
+            for (int j = 0; j < nk; ++j, ++c) {
+                wait(&bars->s_full[t][c & 1], (c >> 1) & 1);
+                if (!ok)
+                    break;
+                const uint32_t tm = tm_s + 64 * (c & 1);
                 float s[64];
-                tmem_ld32_async(tm_s + 64 * h, s);
-                tmem_ld32_async(tm_s + 64 * h + 32, s + 32);
+                tmem_ld32_async(tm, s);
+                tmem_ld32_async(tm + 32, s + 32);
                 tmem_ld_wait();
                 tmem_arrived(s);
                 tmem_arrived(s + 32);
-                const int cut = lim - j * kN - 64 * h;      // columns past it are masked
-                if (__any_sync(0xffffffffu, cut < 63)) {
+                const int cut = lim - j * kN;               // columns past it are masked
+                if (__any_sync(0xffffffffu, cut < kN - 1)) {
 #pragma unroll
                     for (int x = 0; x < 64; ++x)
                         s[x] = x <= cut ? s[x] : -INFINITY;
@@ -643,11 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 t0 = max3(t0, s[60], s[61]);
                 t1 = max3(t1, s[62], s[63]);
-                float top = fmaxf(max3(t0, t1, t2), t3);
-                // the other half's maximum; behind this barrier both have read S, so P may overwrite it
-                s_max[t][j & 1][h][row] = top;
-                named_sync(1 + t, 256);
-                top = fmaxf(top, s_max[t][j & 1][1 - h][row]) * a.c;
+                const float top = fmaxf(max3(t0, t1, t2), t3) * a.c;
                 // the accumulator keeps its old maximum until the new one is 2^8 larger; a warp rescales together
                 float f = 1.0f;
                 if (j == 0 || top > m + kLazy) {
@@ -655,11 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = fmaxf(m, top);
                 }
                 if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                    wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);   // the product before this step still adds to O
                     float x0, x1;
                     unpair(sum, x0, x1);
                     sum = pair(x0 * f, x1 * f);
 #pragma unroll 1
-                    for (int x = 0; x < D / 32; ++x) {
+                    for (int x = 0; x < D / 16; ++x) {
                         uint32_t w[16];
                         float o[16];
                         tmem_ld16(tm_o + 16 * x, o);
@@ -669,29 +622,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(tm_o + 16 * x, w);
                     }
                 }
-                if (tail > 0 && j == nk - 1) {
+                if (j == n - 1 && (it.L & 15) && n * kN > it.L) {
                     // V rows behind the last key, within its group of 16, meet weights of 0 in the product: they may
                     // hold NaN and are zeroed, by the warps of each query tile before they hand over P
                     const uint32_t vs = slot + 2 * j + 1;
                     wait(&bars->kv_full[vs % kStages], (vs / kStages) & 1);
-                    for (int i = 128 * h + row; ok && i < (16 - (tail & 15)) * kHalves * 8; i += 256) {
-                        const int key = tail + i / (kHalves * 8), x = (i >> 3) % kHalves;
-                        *reinterpret_cast<uint4*>(sm + L::kv + (vs % kStages) * L::tile + x * 16384 + key * 128 +
+                    const int left = it.L - j * kN;
+                    for (int i = row; ok && i < (16 - (left & 15)) * kHalves * 8; i += 128) {
+                        const int key = left + i / (kHalves * 8), x = (i >> 3) % kHalves;
+                        *reinterpret_cast<uint4*>(sm + L::kv + (vs % kStages) * L::tile + x * (kN * 128) + key * 128 +
                                                   (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
-                    named_sync(1 + t, 256);
                 }
                 const uint64_t cc = pair(a.c, a.c), off = pair(kBias<kF16> - m, kBias<kF16> - m);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t w[8];
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t w[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float& u = s[16 * x + 2 * i];
-                        float& v = s[16 * x + 2 * i + 1];
+                    for (int i = 0; i < 16; ++i) {
+                        float& u = s[32 * x + 2 * i];
+                        float& v = s[32 * x + 2 * i + 1];
                         const uint64_t e = fma2(pair(u, v), cc, off);
-                        if (i % 4 == 3) {
+                        if (kPoly > 0 && i % kPoly == kPoly - 1) {
                             exp2_pair(e, u, v);
                         } else {
                             float e0, e1;
@@ -701,13 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         w[i] = pack2<kF16>(u, v);
                     }
-                    tmem_st8(tm_s + 32 * h + 8 * x, w);
+                    tmem_st16(tm + 16 * x, w);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&bars->p_ready[t][h]);
+                    mbar_arrive(&bars->p_ready[t][c & 1]);
                 // the sum, off the way of the second product
                 uint64_t a0 = pair(s[0], s[1]), a1 = pair(s[2], s[3]);
 #pragma unroll
@@ -717,49 +670,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 sum = add2(sum, add2(a0, a1));
             }
-            if (nk > 0) {
-                wait(&bars->o_full[t], o_use & 1);
-                ++o_use;
-            }
+            if (nk > 0)
+                wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
             slot += 2 * n;
-            // the row's sum from both halves
+            if (!ok)
+                break;
+            const bool store = row < a.ntok * a.G && tok < it.n, sees = lim >= 0;
+            const int head = it.kvh * a.G + row_head;
+            const int64_t q_row = static_cast<int64_t>(it.q0) + tok;
             float l0, l1;
             unpair(sum, l0, l1);
-            float l = l0 + l1;
-            s_sum[t][r & 1][h][row] = l;
-            named_sync(1 + t, 256);
-            l += s_sum[t][r & 1][1 - h][row];
-            get_item(a, sched, r, it);                      // not kept in registers over the loop
-            const int row_tok = row / a.G, tok = it.tok0 + t * a.ntok + row_tok;
-            const bool store = ok && row < a.ntok * a.G && tok < it.n, sees = lim >= 0;
-            const int head = it.kvh * a.G + row - row_tok * a.G;
-            const int64_t q_row = static_cast<int64_t>(it.q0) + tok;
-            const float inv = sees ? 1.0f / l : 0.0f;
-            if (store && a.lse && h == 0)
+            const float l = l0 + l1, inv = sees ? 1.0f / l : 0.0f;
+            if (store && a.lse)
                 a.lse[q_row * a.Hq + head] = sees ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
-            const int64_t e = q_row * a.out_row_stride + head * a.out_head_stride + (D / 2) * h;
-            // 16 columns at a time: few registers, and O of 0 keys (nothing was written there) times 0 is not formed
+            const int64_t e = q_row * a.out_row_stride + head * a.out_head_stride;
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
-                float o[16];
-                tmem_ld16(tm_o + 16 * x, o);
+                float o[32];
+                tmem_ld32(tm_o + 32 * x, o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 32; ++i)
                     o[i] = sees ? o[i] * inv : 0.0f;
-                if (store) {
-                    if (a.out_dtype == RKV_DTYPE_F32) {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + e + 16 * x);
+                if (!store)
+                    continue;
+                if (a.out_dtype == RKV_DTYPE_F32) {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + e + 32 * x);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + e + 16 * x);
+                    for (int i = 0; i < 8; ++i)
+                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + e + 32 * x);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            dst[i] = make_uint4(pack2<kF16>(o[8 * i], o[8 * i + 1]), pack2<kF16>(o[8 * i + 2], o[8 * i + 3]),
-                                                pack2<kF16>(o[8 * i + 4], o[8 * i + 5]),
-                                                pack2<kF16>(o[8 * i + 6], o[8 * i + 7]));
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_uint4(pack2<kF16>(o[8 * i], o[8 * i + 1]), pack2<kF16>(o[8 * i + 2], o[8 * i + 3]),
+                                            pack2<kF16>(o[8 * i + 4], o[8 * i + 5]),
+                                            pack2<kF16>(o[8 * i + 6], o[8 * i + 7]));
                 }
             }
             // the next item's first product overwrites O: it is ordered behind these loads by p_ready
