@@ -15,8 +15,9 @@
 // signalling in it.  So
 //   - a CTA works on two query tiles of the same kv-head, each with its own MMA issuer and softmax warps, and K and
 //     V tiles serve both (one ring in shared memory, filled by TMA);
-//   - each query tile has two S buffers in TMEM (that is what tiles of 64 keys buy: O of two tiles and four S
-//     buffers fill the 512 columns), so the next S is formed while this one's softmax is at work;
+//   - S and P have TMEM columns of their own (that is what tiles of 64 keys buy: two O of 128 columns, two S of 64 and
+//     four P of 32 fill the 512): the next S is formed as soon as this one is in the softmax warps' registers, and
+//     P V runs beside the next softmax, so neither product is waited for in the steady state;
 //   - one thread owns one row (TMEM lane): no shuffles, and the row's maximum and sum never leave registers;
 //   - the accumulator is only rescaled when a row's maximum grew by more than 2^8: rare after the first tiles, so
 //     almost no step waits for the product before it;
@@ -26,7 +27,7 @@
 // from the last (most keys) to the first, taken in snake order by one persistent CTA per SM.  Everything is
 // derived from the offsets on the device, so a captured graph follows them.
 //
-// Warps: 0 TMA producer, 1 and 2 MMA issuers of query tiles 0 and 1, 4-7 and 8-11 their softmax.
+// Warps: 0 TMA producer, 1 and 2 issue S of query tiles 0 and 1, 3 issues P V of both, 4-7 and 8-11 are their softmax.
 // Every wait is bounded (2 s); one that gives up records RKV_ERR_TIMEOUT, all roles leave their loops, and copies
 // and products in flight are waited for before TMEM is freed.
 #include <cudaTypedefs.h>
@@ -48,9 +49,9 @@ using namespace sm100;
 constexpr int kM = 128;                 // rows of a query tile (TMEM lanes)
 constexpr int kN = 64;                  // keys of a tile
 constexpr int kThreads = 384;
-constexpr uint32_t kTmemCols = 512;     // S (P over it) of query tile t, two buffers: 128 t, 128 t + 64; O: 256 + 128 t
+constexpr uint32_t kTmemCols = 512;     // query tile t: S at 128 t, P (two buffers) at 128 t + 64 and + 96, O at 256 + 128 t
 constexpr float kNone = -1e30f;         // running maximum before any key
-constexpr int kPoly = 4;                // every kPoly-th pair of exponentials goes to the FMA pipes (0: none)
+constexpr int kPoly = 8;                // every kPoly-th pair of exponentials goes to the FMA pipes (0: none)
 constexpr float kLazy = 8.0f;           // the accumulator is rescaled when the maximum grows by 2^8
 
 // Weights are kept times 2^kBias: binary16 then holds them up to 2^(8 + 7) and down to 2^-32 of the largest
@@ -184,6 +185,16 @@ __device__ __forceinline__ bool elect_one()
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+__device__ __forceinline__ void named_sync(int id, int n)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ void named_arrive(int id, int n)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
 // 4-D and 3-D tiled TMA loads (no multicast).
@@ -351,18 +362,21 @@ __device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& s
     return true;
 }
 
+// Output staging of a softmax warp: 32 rows of 64 bytes.
+constexpr uint32_t kStage = 32 * 64;
+
 template <int D>
 struct Layout {
     static constexpr uint32_t qtile = kM * D * 2, tile = kN * D * 2;
-    static constexpr int stages = 8;                          // K and V tiles in turn
-    static constexpr uint32_t q = 0, kv = 2 * qtile, bars = kv + stages * tile;
+    static constexpr int stages = 8;                          // K and V tiles in turn (even: K in the even slots)
+    static constexpr uint32_t q = 0, kv = 2 * qtile, stage = kv + stages * tile, bars = stage + 8 * kStage;
     static constexpr uint32_t alloc = bars + 512 + 1024;
 };
 
 template <int kStages>
 struct Bars {
     uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages];
-    uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], last[2];   // [query tile][buffer]
+    uint64_t s_full[2], s_free[2], p_ready[2][2], pv_done[2][2], last[3];   // [query tile][P buffer]
     uint32_t tmem;
     int abort;
     int issued;                 // ring slots filled so far (producer, at its end)
@@ -388,8 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->q_full[t], 1);
             mbar_init(&bars->q_empty[t], 1);
+            mbar_init(&bars->s_full[t], 1);
+            mbar_init(&bars->s_free[t], 4);
             for (int b = 0; b < 2; ++b) {
-                mbar_init(&bars->s_full[t][b], 1);
                 mbar_init(&bars->p_ready[t][b], 4);
                 mbar_init(&bars->pv_done[t][b], 1);
             }
@@ -397,10 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars->kv_full[i], 1);
-            mbar_init(&bars->kv_empty[i], 2);
+            mbar_init(&bars->kv_empty[i], i % 2 == 0 ? 2 : 1);   // K: both S issuers; V: the P V issuer
         }
         mbar_init(&bars->last[0], 1);
         mbar_init(&bars->last[1], 1);
+        mbar_init(&bars->last[2], 1);
         bars->abort = 0;
         bars->issued = 0;
         fence_mbar_init();
@@ -470,76 +486,86 @@ __global__ void __launch_bounds__(kThreads, 1)
             bars->issued = static_cast<int>(slot);
             bars->q_issued[0] = static_cast<int>(q_use0);
             bars->q_issued[1] = static_cast<int>(q_use1);
-        } else if ((warp == 1 || warp == 2) && elect_one()) {
-            // ---------------- MMA issuers: one thread per query tile t.  Step c (counted over all items) uses buffer c & 1 for S
-            // and, over it, P.  S of step c + 1 is formed before P of step c is waited for; it overwrites P of step c - 1,
-            // so it waits for that product (products into different accumulators are not ordered by their issue).
-            constexpr uint32_t idescO = idesc_f32<kF16>(kM, D) | (1u << 16);   // B (= V) MN-major
+        } else if (warp > 0 && elect_one()) {
+            // ---------------- MMA issuers, one thread each: warps 1 and 2 form S of query tiles 0 and 1, warp 3 P V of both, so
+            // that an S whose buffer has become free never stands behind a P that is not ready.  Steps c of a query tile
+            // are counted over all items; K_j of an item is ring slot `slot` + 2 j, V_j the next.
             constexpr uint32_t kTileDesc = L::tile >> 4;   // descriptors count 16 bytes
-            const int t = warp - 1;
-            const uint64_t q_desc = smem_desc_sw128(q_smem + t * L::qtile), k_desc = smem_desc_sw128(kv_smem),
-                           v_desc = smem_desc_mn(kv_smem);
-            const uint32_t tm_s = tmem + 128 * t, tm_o = tmem + 256 + 128 * t;
-            uint32_t slot = 0, q_use = 0, c = 0;
+            uint32_t slot = 0;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = ok && mbar_wait(bar, parity, abort);
                 return ok;
             };
-            for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
-                const int nk = it.nk(t), n = max(nk, it.nk(1 - t)), last_width = it.last_width(t);
-                // K_j is ring slot `slot` + 2 j, V_j the next
-                for (int j = 0; ok && j <= n; ++j) {
-                    if (j < n) {
-                        const uint32_t ks = (slot + 2 * j) % kStages;
-                        if (!wait(&bars->kv_full[ks], ((slot + 2 * j) / kStages) & 1))
+            if (warp < 3) {
+                const int t = warp - 1;
+                const uint64_t q_desc = smem_desc_sw128(q_smem + t * L::qtile), k_desc = smem_desc_sw128(kv_smem);
+                const uint32_t tm_s = tmem + 128 * t;
+                uint32_t q_use = 0, c = 0;
+                for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
+                    const int nk = it.nk(t), n = max(nk, it.nk(1 - t));
+                    for (int j = 0; j < n; ++j, slot += 2) {
+                        const uint32_t ks = slot % kStages;
+                        if (!wait(&bars->kv_full[ks], (slot / kStages) & 1))
                             break;
-                        if (j < nk) {
-                            // S over the 16-key groups that some row sees.  The first S of an item waits for every
-                            // product of the item before, the others for the one two steps earlier
-                            const uint32_t back = j == 0 ? 1 : 2, cs = c + j;
-                            if (j == 0 && !wait(&bars->q_full[t], q_use++ & 1))
-                                break;
-                            if (cs >= back && !wait(&bars->pv_done[t][(cs - back) & 1], ((cs - back) >> 1) & 1))
-                                break;
-                            const uint32_t width = j + 1 < nk ? kN : last_width;
-                            const uint32_t idesc = idesc_f32<kF16>(kM, 0) | ((width >> 3) << 17);
-                            const uint64_t kd = k_desc + ks * kTileDesc;
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk)
-                                mma_f16(tm_s + 64 * (cs & 1), q_desc + (kk / 4) * ((kM * 128) >> 4) + (kk % 4) * 2,
-                                        kd + (kk / 4) * ((kN * 128) >> 4) + (kk % 4) * 2, idesc, kk > 0 ? 1u : 0u);
-                            mma_commit(&bars->s_full[t][cs & 1]);
-                            mma_commit(&bars->kv_empty[ks]);
-                            if (j + 1 == nk)
-                                mma_commit(&bars->q_empty[t]);
-                        } else {
+                        if (j >= nk) {
                             mbar_arrive(&bars->kv_empty[ks]);      // the other query tile's alone
+                            continue;
                         }
-                    }
-                    if (j > 0) {
-                        const uint32_t vslot = slot + 2 * j - 1, vs = vslot % kStages, cp = c + j - 1;   // V_{j - 1}
-                        if (!wait(&bars->kv_full[vs], (vslot / kStages) & 1))
+                        if (j == 0 && !wait(&bars->q_full[t], q_use++ & 1))
                             break;
-                        if (j - 1 < nk) {
-                            if (!wait(&bars->p_ready[t][cp & 1], (cp >> 1) & 1))
-                                break;
-                            tc_fence_after();
-                            const int groups = (j < nk ? kN : last_width) / 16;
-                            const uint64_t vd = v_desc + vs * kTileDesc;
+                        // P V of step c - 2 has read the P buffer that follows from this S, and S of step c - 1 is in the
+                        // softmax warps' registers
+                        if (c > 1 && !wait(&bars->pv_done[t][c & 1], ((c - 2) >> 1) & 1))
+                            break;
+                        if (c > 0 && !wait(&bars->s_free[t], (c - 1) & 1))
+                            break;
+                        tc_fence_after();
+                        // over the 16-key groups that some row sees
+                        const uint32_t width = j + 1 < nk ? kN : it.last_width(t);
+                        const uint32_t idesc = idesc_f32<kF16>(kM, 0) | ((width >> 3) << 17);
+                        const uint64_t kd = k_desc + ks * kTileDesc;
 #pragma unroll
-                            for (int kk = 0; kk < kN / 16; ++kk)
-                                if (kk < groups)
-                                    mma_f16_ts(tm_o, tm_s + 64 * (cp & 1) + 8 * kk, vd + kk * (2048 >> 4), idescO,
-                                               (j > 1 || kk > 0) ? 1u : 0u);
-                            mma_commit(&bars->pv_done[t][cp & 1]);
-                            mma_commit(&bars->kv_empty[vs]);
-                        } else {
-                            mbar_arrive(&bars->kv_empty[vs]);
-                        }
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_f16(tm_s, q_desc + (kk / 4) * ((kM * 128) >> 4) + (kk % 4) * 2,
+                                    kd + (kk / 4) * ((kN * 128) >> 4) + (kk % 4) * 2, idesc, kk > 0 ? 1u : 0u);
+                        mma_commit(&bars->s_full[t]);
+                        mma_commit(&bars->kv_empty[ks]);
+                        if (j + 1 == nk)
+                            mma_commit(&bars->q_empty[t]);
+                        ++c;
                     }
                 }
-                slot += 2 * n;
-                c += nk;
+            } else {
+                constexpr uint32_t idescO = idesc_f32<kF16>(kM, D) | (1u << 16);   // B (= V) MN-major
+                const uint64_t v_desc = smem_desc_mn(kv_smem);
+                uint32_t c0 = 0, c1 = 0;
+                auto issue_pv = [&](int t, uint32_t c, uint64_t vd, int groups, bool first) {
+                    if (!wait(&bars->p_ready[t][c & 1], (c >> 1) & 1))
+                        return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kN / 16; ++kk)
+                        if (kk < groups)
+                            mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 64 + 32 * (c & 1) + 8 * kk,
+                                       vd + kk * (2048 >> 4), idescO, (first && kk == 0) ? 0u : 1u);
+                    mma_commit(&bars->pv_done[t][c & 1]);
+                };
+                for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
+                    const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1);
+                    for (int j = 0; j < n; ++j, slot += 2) {
+                        const uint32_t vs = (slot + 1) % kStages;
+                        if (!wait(&bars->kv_full[vs], ((slot + 1) / kStages) & 1))
+                            break;
+                        const uint64_t vd = v_desc + vs * kTileDesc;
+                        if (j < n0)
+                            issue_pv(0, c0++, vd, (j + 1 < n0 ? kN : it.last_width(0)) / 16, j == 0);
+                        if (j < n1)
+                            issue_pv(1, c1++, vd, (j + 1 < n1 ? kN : it.last_width(1)) / 16, j == 0);
+                        if (!ok)
+                            break;
+                        mma_commit(&bars->kv_empty[vs]);
+                    }
+                }
             }
             if (!ok) {
                 if (!*abort)
@@ -548,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every product that this thread issued has completed before TMEM is released
             volatile int never = 0;
-            mma_commit(&bars->last[t]);
-            mbar_wait(&bars->last[t], 0, &never);
+            mma_commit(&bars->last[warp - 1]);
+            mbar_wait(&bars->last[warp - 1], 0, &never);
         }
     } else {
         // ---------------- softmax: thread = row of query tile t = TMEM lane
@@ -557,6 +583,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tm_s = tmem + 128 * t + lane_off, tm_o = tmem + 256 + 128 * t + lane_off;
         const int row_tok = row / a.G, row_head = row - row_tok * a.G;
+        // The warps of the two query tiles that share a scheduler take turns at their exponentials: each then has the
+        // special-function unit to itself while the other waits for S, finds its maximum or stores.
+        const int my_turn = 1 + 2 * (warp & 3) + t, other_turn = 1 + 2 * (warp & 3) + 1 - t;
         uint32_t c = 0, slot = 0;                           // steps of this query tile, ring slots
         bool ok = true;
         Item it;
@@ -565,23 +594,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, got);
             tc_fence_after();
         };
-        for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
+        if (t == 1)
+            named_arrive(other_turn, 64);
+        // after a wait gave up the loops go on without work, so that the turns stay matched
+        for (int r = 0; get_item(a, sched, r, it); ++r) {
             const int nk = it.nk(t), tok = it.tok0 + t * a.ntok + row_tok;
             const int lim = it.L - it.n + tok;              // last key that this row sees
             const int n = max(nk, it.nk(1 - t));
             float m = kNone;
             uint64_t sum = pair(0.0f, 0.0f);
             for (int j = 0; j < nk; ++j, ++c) {
-                wait(&bars->s_full[t][c & 1], (c >> 1) & 1);
-                if (!ok)
-                    break;
-                const uint32_t tm = tm_s + 64 * (c & 1);
+                wait(&bars->s_full[t], c & 1);
                 float s[64];
-                tmem_ld32_async(tm, s);
-                tmem_ld32_async(tm + 32, s + 32);
+                tmem_ld32_async(tm_s, s);
+                tmem_ld32_async(tm_s + 32, s + 32);
                 tmem_ld_wait();
                 tmem_arrived(s);
                 tmem_arrived(s + 32);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&bars->s_free[t]);          // the next S may be formed
                 const int cut = lim - j * kN;               // columns past it are masked
                 if (__any_sync(0xffffffffu, cut < kN - 1)) {
 #pragma unroll
@@ -600,19 +633,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t0 = max3(t0, s[60], s[61]);
                 t1 = max3(t1, s[62], s[63]);
                 const float top = fmaxf(max3(t0, t1, t2), t3) * a.c;
-                // the accumulator keeps its old maximum until the new one is 2^8 larger; a warp rescales together
-                float f = 1.0f;
-                if (j == 0 || top > m + kLazy) {
-                    f = ex2(m - top);
-                    m = fmaxf(m, top);
-                }
-                if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-                    wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);   // the product before this step still adds to O
+                // the accumulator keeps its old maximum until the new one is 2^8 larger (the first tile counts as such);
+                // a warp rescales together
+                if (__any_sync(0xffffffffu, top > m + kLazy)) {
+                    const float was = m;
+                    m = top > m + kLazy ? top : m;
+                    const float f = ex2(was - m);
+                    // the product before this step still adds to O
+                    if (j > 0)
+                        wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
                     float x0, x1;
                     unpair(sum, x0, x1);
                     sum = pair(x0 * f, x1 * f);
 #pragma unroll 1
-                    for (int x = 0; x < D / 16; ++x) {
+                    for (int x = 0; j > 0 && x < D / 16; ++x) {
                         uint32_t w[16];
                         float o[16];
                         tmem_ld16(tm_o + 16 * x, o);
@@ -635,15 +669,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
+                const uint32_t tm_p = tm_s + 64 + 32 * (c & 1);
                 const uint64_t cc = pair(a.c, a.c), off = pair(kBias<kF16> - m, kBias<kF16> - m);
+                uint64_t a0 = pair(0.0f, 0.0f), a1 = a0;
+                named_sync(my_turn, 64);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float& u = s[32 * x + 2 * i];
-                        float& v = s[32 * x + 2 * i + 1];
-                        const uint64_t e = fma2(pair(u, v), cc, off);
+                        const uint64_t e = fma2(pair(s[32 * x + 2 * i], s[32 * x + 2 * i + 1]), cc, off);
+                        float u, v;
                         if (kPoly > 0 && i % kPoly == kPoly - 1) {
                             exp2_pair(e, u, v);
                         } else {
@@ -653,29 +689,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                             v = ex2(e1);
                         }
                         w[i] = pack2<kF16>(u, v);
+                        if (i & 1)
+                            a1 = add2(a1, pair(u, v));
+                        else
+                            a0 = add2(a0, pair(u, v));
                     }
-                    tmem_st16(tm + 16 * x, w);
+                    tmem_st16(tm_p + 16 * x, w);
                 }
+                named_arrive(other_turn, 64);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bars->p_ready[t][c & 1]);
-                // the sum, off the way of the second product
-                uint64_t a0 = pair(s[0], s[1]), a1 = pair(s[2], s[3]);
-#pragma unroll
-                for (int x = 4; x < 64; x += 4) {
-                    a0 = add2(a0, pair(s[x], s[x + 1]));
-                    a1 = add2(a1, pair(s[x + 2], s[x + 3]));
-                }
                 sum = add2(sum, add2(a0, a1));
+            }
+            for (int j = nk; j < n; ++j) {                  // steps of the other query tile alone
+                named_sync(my_turn, 64);
+                named_arrive(other_turn, 64);
             }
             if (nk > 0)
                 wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
             slot += 2 * n;
-            if (!ok)
-                break;
-            const bool store = row < a.ntok * a.G && tok < it.n, sees = lim >= 0;
+            const bool store = ok && row < a.ntok * a.G && tok < it.n, sees = lim >= 0;
             const int head = it.kvh * a.G + row_head;
             const int64_t q_row = static_cast<int64_t>(it.q0) + tok;
             float l0, l1;
@@ -683,33 +719,50 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float l = l0 + l1, inv = sees ? 1.0f / l : 0.0f;
             if (store && a.lse)
                 a.lse[q_row * a.Hq + head] = sees ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
-            const int64_t e = q_row * a.out_row_stride + head * a.out_head_stride;
+            // Rows go out through a small staging area of the warp, 64 bytes of each at a time, so that four lanes store
+            // neighbouring pieces of one row (a lane storing its own row touches 32 lines per instruction: 4800 cycles
+            // an item).  16-byte pieces are swizzled by the row against bank conflicts.
+            const uint32_t rows = __ballot_sync(0xffffffffu, store);
+            const int64_t row_at = q_row * a.out_row_stride + head * a.out_head_stride;   // elements
+            unsigned char* st = sm + L::stage + (warp - 4) * kStage;
+            const bool f32 = a.out_dtype == RKV_DTYPE_F32;
+            const int chunk = f32 ? 16 : 32;                // columns of 64 bytes
 #pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
-                float o[32];
-                tmem_ld32(tm_o + 32 * x, o);
+            for (int x = 0; rows != 0 && x < D; x += chunk) {
+                uint32_t w[16];
+                if (f32) {
+                    float o[16];
+                    tmem_ld16(tm_o + x, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = sees ? o[i] * inv : 0.0f;
-                if (!store)
-                    continue;
-                if (a.out_dtype == RKV_DTYPE_F32) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + e + 32 * x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = __float_as_uint(sees ? o[i] * inv : 0.0f);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + e + 32 * x);
+                    float o[32];
+                    tmem_ld32(tm_o + x, o);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(pack2<kF16>(o[8 * i], o[8 * i + 1]), pack2<kF16>(o[8 * i + 2], o[8 * i + 3]),
-                                            pack2<kF16>(o[8 * i + 4], o[8 * i + 5]),
-                                            pack2<kF16>(o[8 * i + 6], o[8 * i + 7]));
+                    for (int i = 0; i < 16; ++i)
+                        w[i] = sees ? pack2<kF16>(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(st + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int src = 8 * i + (lane >> 2), piece = lane & 3;   // row of the warp, 16 bytes of its 64
+                    const uint4 v = *reinterpret_cast<const uint4*>(st + src * 64 + ((piece ^ ((src >> 1) & 3)) << 4));
+                    const int64_t at = __shfl_sync(0xffffffffu, row_at, src) + x;
+                    if (rows >> src & 1u)
+                        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.out) + at * (f32 ? 4 : 2) + 16 * piece) = v;
+                }
+                __syncwarp();
             }
             // the next item's first product overwrites O: it is ordered behind these loads by p_ready
             tc_fence_before();
         }
+        if (t == 0)
+            named_sync(my_turn, 64);                        // the turn that the other warp still passes on
         if (!ok && lane == 0) {
             if (!*abort)
                 report(a.err, RKV_ERR_TIMEOUT);
