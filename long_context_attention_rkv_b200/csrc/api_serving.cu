@@ -205,7 +205,7 @@ rkv_status rkv_kv8_store(const rkv_kv8_cache* cache, const void* K_new, const vo
         return RKV_OK;
     if (!K_new || !V_new || !aligned(K_new, 16) || !aligned(V_new, 16) || !ints_ok(slot_map))
         return RKV_ERR_INVALID_ARG;
-    if (n_rows * cache->n_kv_heads > INT32_MAX)
+    if (n_rows > INT32_MAX / cache->n_kv_heads)
         return RKV_ERR_UNSUPPORTED;
     int sms = 0;
     s = device_sms(&sms);

@@ -7,11 +7,11 @@
 // new_c) gets slot table[b][p / s] * s + p % s.  Giving back is the reverse: the blocks of the ended
 // requests go on the stack in request order.
 //
-// One launch each.  Every CTA reads all lengths (at most 256) and forms both prefix sums itself, in
-// shared memory, so nothing has to be handed over between kernels; the CTAs then share the output
-// entries.  They form one cluster, whose barrier separates the last read of the lengths and of the
-// stack's height from the first write, so both may be updated in place.  A token finds its request
-// by a binary search of the prefix sums (8 steps in shared memory).
+// Every CTA reads all lengths (at most 256) and forms the prefix sums itself, in shared memory, so nothing is
+// handed over between CTAs; they share the output entries.  A token finds its request by a binary search of the
+// prefix sums (8 steps in shared memory).  The lengths and the stack's height may be updated in place, so they
+// are written when every CTA has read them: by the only CTA of a small call, behind a cluster's barrier
+// (giving back), or by a small second launch (prompts).
 #include <cooperative_groups.h>
 
 #include "device_common.cuh"
@@ -24,6 +24,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024;
+constexpr int kMaxCtas = 128;
 static_assert(kThreads >= RKV_MAX_BATCH, "one thread per request in the prefix sums");
 
 constexpr int kScanWarps = RKV_MAX_BATCH / 32;
@@ -79,23 +80,19 @@ struct BlockShared {
     int bad;                       // smallest status that forbids the call (kNone: none)
 };
 
-// kPer: neighbouring tokens per thread and round.  Four almost always share a request and a block, so one search
-// and one lookup serve them (a prompt of 196608 tokens: 23.6 -> 13.7 us); in a decode step every token is another
-// request's and one per thread keeps the lookups side by side (256 requests: 7.8 -> 4.5 us).
-template <int kPer>
-__global__ void __launch_bounds__(kThreads)
-    blocks_extend_kernel(const rkv_blocks_config c, int shift, const int32_t* lengths, const int32_t* new_counts,
-                         int32_t* table, const int32_t* __restrict__ free_list, const int32_t* n_free,
-                         int32_t* new_off, int32_t* slot_map, int64_t max_new, int32_t* lengths_out,
-                         int32_t* n_free_out, int32_t* err)
+// What rkv_blocks_extend does, from the lengths (whole CTA): the prefix sums in s, s.bad, and for its request each
+// thread's held and new tokens.  Returns the stack's height.
+__device__ __forceinline__ int plan_extend(const rkv_blocks_config& c, int shift, const int32_t* lengths,
+                                           const int32_t* new_counts, const int32_t* n_free, int64_t max_new,
+                                           BlockShared& s, int64_t& len, int64_t& add)
 {
-    __shared__ BlockShared s;
     const int tid = threadIdx.x;
     if (tid == 0)
         s.bad = kNone;
     __syncthreads();
     const int nfree = *n_free;
-    int64_t len = 0, add = 0, have = 0, more = 0;
+    int64_t have = 0, more = 0;
+    len = add = 0;
     if (tid < c.batch) {
         len = lengths[tid];
         add = new_counts[tid];
@@ -104,7 +101,7 @@ __global__ void __launch_bounds__(kThreads)
         have = (len + m) >> shift;
         if (len < 0 || add < 0) {
             atomicMin(&s.bad, RKV_ERR_INVALID_ARG);
-            len = add = have = 0;
+            add = have = 0;
         } else if (need > c.max_blocks) {
             atomicMin(&s.bad, RKV_ERR_WORKSPACE);
             add = 0;
@@ -129,45 +126,55 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (tid == c.batch - 1 && (tok > max_new || blk > nfree))
         atomicMin(&s.bad, RKV_ERR_WORKSPACE);
-    // every CTA has read lengths and n_free: from here on they may be overwritten
-    cg::this_cluster().sync();
+    __syncthreads();   // also: this CTA has read lengths and n_free
+    return nfree;
+}
+
+// The new lengths and the stack's height (one CTA, after plan_extend).
+__device__ __forceinline__ void write_lengths(const rkv_blocks_config& c, const BlockShared& s, int nfree, int64_t len,
+                                              int64_t add, int32_t* lengths_out, int32_t* n_free_out, int32_t* err)
+{
+    const bool ok = s.bad == kNone;
+    if (threadIdx.x < c.batch)
+        lengths_out[threadIdx.x] = static_cast<int>(ok ? len + add : len);
+    if (threadIdx.x == 0) {
+        *n_free_out = nfree - (ok ? s.more[c.batch] : 0);
+        if (!ok)
+            report(err, s.bad);
+    }
+}
+
+// kPer: neighbouring tokens per thread and round.  Four almost always share a request and a block, so one search
+// and one lookup serve them; in a decode step every token is another request's and one per thread keeps the lookups
+// side by side.  kAlone: one CTA, which also writes the new lengths; otherwise another launch does that, when
+// every CTA of this one has read the old ones.
+template <int kPer, bool kAlone>
+__global__ void __launch_bounds__(kThreads)
+    blocks_extend_kernel(const rkv_blocks_config c, int shift, const int32_t* lengths, const int32_t* new_counts,
+                         int32_t* table, const int32_t* __restrict__ free_list, const int32_t* n_free,
+                         int32_t* new_off, int32_t* slot_map, int64_t max_new, int32_t* lengths_out,
+                         int32_t* n_free_out, int32_t* err)
+{
+    __shared__ BlockShared s;
+    const int tid = threadIdx.x;
+    int64_t len, add;
+    const int nfree = plan_extend(c, shift, lengths, new_counts, n_free, max_new, s, len, add);
+    if constexpr (kAlone)
+        write_lengths(c, s, nfree, len, add, lengths_out, n_free_out, err);
 
     const int gtid = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
-    if (s.bad != kNone) {
-        for (int64_t t = gtid; t < max_new; t += gsize)
-            slot_map[t] = -1;
-        if (blockIdx.x == 0) {
-            if (tid < c.batch) {
-                new_off[tid + 1] = 0;
-                lengths_out[tid] = lengths[tid];
-            }
-            if (tid == 0) {
-                new_off[0] = 0;
-                *n_free_out = nfree;
-                report(err, s.bad);
-            }
-        }
-        return;
-    }
-    const int total = s.off[c.batch], taken = s.more[c.batch];
-    if (blockIdx.x == 0) {
-        if (tid < c.batch) {
-            new_off[tid + 1] = s.off[tid + 1];
-            lengths_out[tid] = static_cast<int>(len + add);
-        }
-        if (tid == 0) {
-            new_off[0] = 0;
-            *n_free_out = nfree - taken;
-        }
-    }
+    const bool ok = s.bad == kNone;
+    const int total = ok ? s.off[c.batch] : 0, taken = ok ? s.more[c.batch] : 0;
+    if (blockIdx.x == 0 && tid <= c.batch)
+        new_off[tid] = ok ? s.off[tid] : 0;
     bool corrupt = false;
     for (int i = gtid; i < taken; i += gsize) {
         const int b = owner(s.more, c.batch, i);
         table[static_cast<int64_t>(b) * c.max_blocks + s.have[b] + i - s.more[b]] = free_list[nfree - 1 - i];
     }
-    const bool wide = kPer == 4 && (reinterpret_cast<uintptr_t>(slot_map) & 15) == 0;
+    const bool wide = kPer % 4 == 0 && (reinterpret_cast<uintptr_t>(slot_map) & 15) == 0;
     for (int64_t t0 = static_cast<int64_t>(kPer) * gtid; t0 < max_new; t0 += static_cast<int64_t>(kPer) * gsize) {
-        int slot[4], b = 0, ord = -1, id = -1;
+        int slot[kPer], b = 0, ord = -1, id = -1;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int64_t t = t0 + i;
@@ -193,7 +200,9 @@ __global__ void __launch_bounds__(kThreads)
                 slot[i] = (id << shift) + (p & ((1 << shift) - 1));
         }
         if (wide && t0 + kPer <= max_new) {
-            *reinterpret_cast<int4*>(slot_map + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+#pragma unroll
+            for (int i = 0; i + 3 < kPer; i += 4)
+                *reinterpret_cast<int4*>(slot_map + t0 + i) = make_int4(slot[i], slot[i + 1], slot[i + 2], slot[i + 3]);
         } else {
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
@@ -203,6 +212,18 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (corrupt)
         report(err, RKV_ERR_CORRUPT);
+}
+
+// The new lengths, after the CTAs of blocks_extend_kernel<., false>.
+__global__ void __launch_bounds__(kThreads)
+    blocks_lengths_kernel(const rkv_blocks_config c, int shift, const int32_t* lengths, const int32_t* new_counts,
+                          const int32_t* n_free, int64_t max_new, int32_t* lengths_out, int32_t* n_free_out, int32_t* err)
+{
+    __shared__ BlockShared s;
+    int64_t len, add;
+    const int nfree = plan_extend(c, shift, lengths, new_counts, n_free, max_new, s, len, add);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    write_lengths(c, s, nfree, len, add, lengths_out, n_free_out, err);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -269,8 +290,7 @@ int log2_of(int n)
     return s;
 }
 
-// CTAs (one cluster) for `work` output entries: one CTA covers a decode step (a few hundred
-// entries) in one round; eight, the largest portable cluster, share a prompt's tens of thousands.
+// CTAs (one cluster) for `work` output entries, 4 per thread and round in one CTA, else the largest portable cluster.
 int cluster_for(int64_t work) { return work <= 4 * kThreads ? 1 : 8; }
 
 template <typename... KArgs, typename... Args>
@@ -297,10 +317,33 @@ cudaError_t launch_blocks_extend(const rkv_blocks_config& c, const int32_t* leng
                                  int32_t* slot_map, int64_t max_new, int32_t* lengths_out, int32_t* n_free_out,
                                  int32_t* err, cudaStream_t st)
 {
-    // up to one token per thread: a decode step
-    return launch_cluster(max_new <= kThreads ? blocks_extend_kernel<1> : blocks_extend_kernel<4>, cluster_for(max_new),
-                          st, c, log2_of(c.block_size), lengths, new_counts, table, free_list, n_free, new_off,
-                          slot_map, max_new, lengths_out, n_free_out, err);
+    const int shift = log2_of(c.block_size);
+    if (max_new <= 4 * kThreads) {
+        // one CTA; up to one token per thread: a decode step
+        auto kern = max_new <= kThreads ? blocks_extend_kernel<1, true> : blocks_extend_kernel<4, true>;
+        kern<<<1, kThreads, 0, st>>>(c, shift, lengths, new_counts, table, free_list, n_free, new_off, slot_map, max_new,
+                                     lengths_out, n_free_out, err);
+        return cudaGetLastError();
+    }
+    // one round of 4 tokens per thread, at most kMaxCtas CTAs.  196608 slots: 5.7 us with both launches; one cluster of
+    // eight CTAs, whose barrier would save the second launch, takes 12.3 us
+    const int64_t ctas = (max_new + 4 * kThreads - 1) / (4 * kThreads);
+    blocks_extend_kernel<4, false><<<static_cast<unsigned>(ctas < kMaxCtas ? ctas : kMaxCtas), kThreads, 0, st>>>(
+        c, shift, lengths, new_counts, table, free_list, n_free, new_off, slot_map, max_new, lengths_out, n_free_out, err);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, blocks_lengths_kernel, c, shift, lengths, new_counts, n_free, max_new, lengths_out,
+                              n_free_out, err);
 }
 
 cudaError_t launch_blocks_release(const rkv_blocks_config& c, const int32_t* lengths, const int32_t* ended,

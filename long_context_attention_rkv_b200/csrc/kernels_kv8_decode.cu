@@ -47,7 +47,7 @@ using namespace kv8;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;     // tokens per CTA step
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 4;
 constexpr int kMaxCtas = 160 * kCtasPerSm;
 constexpr float kNone = -1e30f;        // running maximum before any token
 constexpr float kWeightExp = 15.0f;    // weights are kept times 2^15: binary16 then holds 2^-39 .. 1 of the largest
@@ -269,6 +269,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
         const int32_t* row = a.table + static_cast<int64_t>(b) * a.max_blocks;
         const uint16_t* qu = a.q + (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kvh) * a.G) * D;
 
+        // This warp's 16 tokens of each tile.  The next tile's K codes are loaded as soon as this one's are in
+        // the products, its V codes likewise, and its block id a tile earlier: loads stay in flight all
+        // the time without a second set of registers.
+        const int tok_mask = (1 << a.block_shift) - 1;
+        auto block_id = [&](int ti) {
+            const int tok = ti * kTile + warp * 16;
+            return tok < len && ti < t_hi ? __ldg(row + (tok >> a.block_shift)) : 0;
+        };
+        auto checked = [&](int id) {
+            const bool bad = id < 0 || id >= a.n_blocks;
+            corrupt |= bad;
+            return bad ? -1 : id;
+        };
+        Codes<D> c;
+        int id = checked(block_id(t_lo)), next_id = block_id(t_lo + 1);
+        c.load_k(a, id, (t_lo * kTile + warp * 16) & tok_mask, kvh, lane);
+        c.load_v(a, id, (t_lo * kTile + warp * 16) & tok_mask, kvh, lane);
+
         // ---- q as B operands: lane (g, t) holds head 8 n + g, the channels of its K pieces
         uint32_t qf[NT][kSteps][2];
 #pragma unroll
@@ -329,23 +347,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             l[n][0] = l[n][1] = 0.0f;
         }
 
-        // This warp's 16 tokens of each tile.  The next tile's K codes are loaded as soon as this one's are in
-        // the products, its V codes likewise, and its block id a tile earlier: loads stay in flight all
-        // the time without a second set of registers.
-        const int tok_mask = (1 << a.block_shift) - 1;
-        auto block_id = [&](int ti) {
-            const int tok = ti * kTile + warp * 16;
-            return tok < len && ti < t_hi ? __ldg(row + (tok >> a.block_shift)) : 0;
-        };
-        auto checked = [&](int id) {
-            const bool bad = id < 0 || id >= a.n_blocks;
-            corrupt |= bad;
-            return bad ? -1 : id;
-        };
-        Codes<D> c;
-        int id = checked(block_id(t_lo)), next_id = block_id(t_lo + 1);
-        c.load_k(a, id, (t_lo * kTile + warp * 16) & tok_mask, kvh, lane);
-        c.load_v(a, id, (t_lo * kTile + warp * 16) & tok_mask, kvh, lane);
         for (int ti = t_lo; ti < t_hi; ++ti) {
             const int tok = ti * kTile + warp * 16;
             if (tok >= len)
@@ -524,6 +525,16 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, 
         return;
     // part i: the unit's first CTA left its tail slot, the others their head slots
     auto slot = [&](int i) { return (static_cast<int64_t>(2 * (pa + i)) + (i == 0 ? 1 : 0)) * a.G + head; };
+    // the first parts' outputs are on their way while the factors are formed
+    constexpr int kAhead = 4;
+    const int row = tid / kLanes, col = tid % kLanes;
+    float4 first[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = row + k * kRows;
+        first[k] = i < np ? __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D) + col)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     float M = kNone;
     for (int i = tid; i < np; i += kThreads)
         M = fmaxf(M, __ldcg(&a.part_ml[slot(i)]).x);
@@ -549,10 +560,17 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, 
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
         L += s_r[1][w];
-    const int row = tid / kLanes, col = tid % kLanes;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const float f = row + k * kRows < np ? s_f[row + k * kRows] : 0.0f;
+        o.x = fmaf(first[k].x, f, o.x);
+        o.y = fmaf(first[k].y, f, o.y);
+        o.z = fmaf(first[k].z, f, o.z);
+        o.w = fmaf(first[k].w, f, o.w);
+    }
 #pragma unroll 4
-    for (int i = row; i < np; i += kRows) {
+    for (int i = row + kAhead * kRows; i < np; i += kRows) {
         const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D) + col);
         const float f = s_f[i];
         o.x = fmaf(v.x, f, o.x);

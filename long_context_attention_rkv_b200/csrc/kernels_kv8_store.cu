@@ -16,10 +16,9 @@
 // eight 16-byte pieces of a full block: small CTAs, many of them per SM, keep loads in flight while others
 // reduce and convert.
 //
-// The quotient x / s decides the code through its rounding, so it must be the correctly rounded one; but
-// x * fl(1 / s) is within 3 half steps (2^-22.4) of x / s, so the rounding can only differ if that product
-// lies within 2^-20 (relative) of a border between two codes.  Only then (and in the floats' subnormal
-// range) is the division done.
+// The code is that of the correctly rounded quotient x / s.  x * r with r = fl(1 / s) is within 2^-22 (relative) of
+// it, so x * r (1 - 2^-21) and x * r (1 + 2^-21) enclose it; rounding to codes is monotone, so where both give the
+// same code that is the quotient's.  The division is done only for a piece of eight values where they differ.
 #include <cfloat>
 
 #include "kv8_common.cuh"
@@ -80,54 +79,86 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red)
     return m;
 }
 
-// Eight codes of x / s: r = fl(1 / s); exact: every quotient by division.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_pair(uint64_t v)
+{
+    float x, y;
+    unpair(v, x, y);
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Eight codes by division; rare, and kept out of line so that it takes no registers from the common path.
 template <bool kE4M3>
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, float r, bool exact)
+__device__ __noinline__ uint2 divide8(float4 a, float4 b, float s)
+{
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t o[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        o[e >> 2] |= encode<kE4M3>(__fdiv_rn(x[e], s)) << (8 * (e & 3));
+    return make_uint2(o[0], o[1]);
+}
+
+// Eight codes of x / s; lo, hi: pairs of the factors that enclose 1 / s.  exact: by division whatever they say.
+template <bool kE4M3>
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, uint64_t lo, uint64_t hi, bool exact)
 {
     uint32_t o[2];
-    float t[8];
     if constexpr (kE4M3) {
-        // border between two normal codes: the 20 bits under the three kept ones are 0x80000
-        uint32_t dist = 0xffffffffu;
-        float small = FLT_MAX;
+        uint32_t p[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            t[e] = __fmul_rn(x[e], r);
-            dist = min(dist, (__float_as_uint(t[e]) - 0x7fff8u) & 0xfffffu);
-            small = fminf(small, fabsf(t[e]));
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t a = pair(x[4 * i], x[4 * i + 1]), b = pair(x[4 * i + 2], x[4 * i + 3]);
+            o[i] = e4m3_pair(mul2(a, lo)) | (e4m3_pair(mul2(b, lo)) << 16);
+            p[i] = e4m3_pair(mul2(a, hi)) | (e4m3_pair(mul2(b, hi)) << 16);
         }
-        exact |= dist <= 16u || small < 0x1p-6f;
+        exact |= o[0] != p[0] || o[1] != p[1];
     } else {
-        // t + 1.5 2^23 holds rint(t) in its low bits
-        float far = 0.0f;
+        // x * f + 1.5 2^23, rounded once, holds rint(x * f) in its low bits
+        const uint64_t magic = pair(12582912.0f, 12582912.0f);
         uint32_t u[8];
+        uint64_t differ = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            t[e] = __fmul_rn(x[e], r);
-            const float m = __fadd_rn(t[e], 12582912.0f);
-            far = fmaxf(far, fabsf(t[e] - (m - 12582912.0f)));
-            u[e] = __float_as_uint(m);
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t a = pair(x[2 * i], x[2 * i + 1]);
+            const uint64_t l = fma2(a, lo, magic);
+            differ |= l ^ fma2(a, hi, magic);
+            u[2 * i] = static_cast<uint32_t>(l);
+            u[2 * i + 1] = static_cast<uint32_t>(l >> 32);
         }
-        exact |= far > 0.5f - 0x1p-14f;
+        exact |= differ != 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             o[i] = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040), __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040),
                                0x5410);
     }
-    if (exact) {
-        o[0] = o[1] = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            o[e >> 2] |= encode<kE4M3>(__fdiv_rn(x[e], s)) << (8 * (e & 3));
-    } else if constexpr (kE4M3) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i], t[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * i + 2], t[4 * i + 3]), __NV_SATFINITE,
-                                                         __NV_E4M3);
-            o[i] = lo | (hi << 16);
-        }
-    }
+    if (exact)
+        return divide8<kE4M3>(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), s);
     return make_uint2(o[0], o[1]);
 }
 
@@ -150,7 +181,7 @@ __device__ __forceinline__ int doublings(float was, float need)
 __device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 template <int D, int kThreads, bool kE4M3, bool kF16>
-__global__ void __launch_bounds__(kThreads, 768 / kThreads) kv8_store_kernel(const StoreArgs a)
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv8_store_kernel(const StoreArgs a)
 {
     constexpr int kCols = D / 8;                                   // 16-byte pieces of an input row
     constexpr int kPieces = 8;                                     // per thread, for a full block
@@ -164,6 +195,8 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) kv8_store_kernel(con
     const int64_t w0 = static_cast<int64_t>(blockIdx.x / a.Hkv) * a.window;
     const int mask = (1 << a.shift) - 1, near = a.window + mask + 1;
     const int64_t pool = static_cast<int64_t>(a.n_blocks) << a.shift;
+
+    const uint16_t* x = (side ? a.x[1] : a.x[0]) + h * a.head_stride;
 
     // ---- the runs that start in this window
     bool corrupt = false;
@@ -191,7 +224,6 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) kv8_store_kernel(con
     }
     __syncthreads();
 
-    const uint16_t* x = a.x[side] + h * a.head_stride;
     for (int word = 0; word * 32 < a.window; ++word) {
         for (uint32_t left = starts[word]; left; left &= left - 1) {
             const int i = word * 32 + __ffs(left) - 1;
@@ -207,8 +239,8 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) kv8_store_kernel(con
             n = min(n, mask + 1);
             const int slot = sl[i + 1], blk = slot >> a.shift, off = slot & mask;
             const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + h;
-            uint8_t* codes = a.codes[side] + (unit << a.shift) * D;
-            float* scale = a.scale[side] + unit;
+            uint8_t* codes = (side ? a.codes[1] : a.codes[0]) + (unit << a.shift) * D;
+            float* scale = (side ? a.scale[1] : a.scale[0]) + unit;
 
             // ---- the rows, and the largest |x|
             uint4 v[kPieces];
@@ -280,6 +312,8 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) kv8_store_kernel(con
 
             // ---- the new codes
             const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            const float r_lo = __fmul_rn(r, 1.0f - 0x1p-21f), r_hi = __fmul_rn(r, 1.0f + 0x1p-21f);
+            const uint64_t lo = pair(r_lo, r_lo), hi = pair(r_hi, r_hi);
             exact |= s < kMinScale;
             uint8_t* dst = codes + (off + tid / kCols) * D + (tid % kCols) * 8;
 #pragma unroll
@@ -287,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) kv8_store_kernel(con
                 if (tid + j * kThreads < n * kCols) {
                     float f[8];
                     widen<kF16>(v[j], f);
-                    const uint2 o = s > 0.0f ? quantise8<kE4M3>(f, s, r, exact) : make_uint2(0, 0);
+                    const uint2 o = s > 0.0f ? quantise8<kE4M3>(f, s, lo, hi, exact) : make_uint2(0, 0);
                     *reinterpret_cast<uint2*>(dst + j * (kThreads / kCols) * D) = o;
                 }
             }
