@@ -488,8 +488,8 @@ typedef struct rkv_prefill_config {
  *            outside q or K is skipped and RKV_ERR_INVALID_ARG recorded there (the first error stays); a
  *            bounded wait that ran out records RKV_ERR_TIMEOUT
  * Rows of K and V outside a sequence's keys may hold anything (NaN too) and do not reach it, but a
- * plane's kv_rows rows must be readable.  A non-finite key or value inside a sequence may reach
- * earlier rows of the same 128 keys too.  q, K, V 16-byte aligned.  q, K, V must not overlap out or lse.
+ * plane's kv_rows rows must be readable.  Inside a sequence a NaN key reaches the rows that see it and no
+ * others; a non-finite value may reach earlier rows of the same 64 keys too.  q, K, V 16-byte aligned.  q, K, V must not overlap out or lse.
  * Softmax statistics and sums are 32-bit; the weights enter the second product in in_dtype.  No
  * workspace; calls on any streams may overlap.
  */

@@ -50,7 +50,7 @@ constexpr int kM = 128;                 // rows of a query tile (TMEM lanes)
 constexpr int kN = 64;                  // keys of a tile
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;     // query tile t: S at 128 t, P (two buffers) at 128 t + 64 and + 96, O at 256 + 128 t
-constexpr float kNone = -1e30f;         // running maximum before any key
+constexpr float kNone = -FLT_MAX;       // running maximum before any key
 constexpr int kPoly = 8;                // every kPoly-th pair of exponentials goes to the FMA pipes (0: none)
 constexpr float kLazy = 8.0f;           // the accumulator is rescaled when the maximum grows by 2^8
 
@@ -78,10 +78,11 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
+// The largest of three, NaN if one of them is.
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -115,12 +116,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 
 // 2^x of a pair on the FMA pipes, x <= 2^6: x = n + f with n = rint(x) (taken from the low bits of x + 1.5 2^23),
 // 2^f by the degree-5 polynomial of least relative error on [-1/2, 1/2] (found by the Remez exchange; 7.5e-8, with
-// fp32 rounding under 2^-22), n added to the exponent field.  x is held at -125, where a weight no longer counts.
+// fp32 rounding under 2^-22), n added to the exponent field.  x is held at -127, where that leaves 0 or one of the
+// smallest subnormal steps: nothing in the weight's 16 bits.
 __device__ __forceinline__ void exp2_pair(uint64_t x, float& r0, float& r1)
 {
     float a, b;
     unpair(x, a, b);
-    x = pair(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
+    x = pair(fmaxf(a, -127.0f), fmaxf(b, -127.0f));
     const uint64_t magic = pair(12582912.0f, 12582912.0f), back = pair(-12582912.0f, -12582912.0f);
     const uint64_t t = add2(x, magic);
     const uint64_t f = fma2(add2(t, back), pair(-1.0f, -1.0f), x);
@@ -600,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = 0; get_item(a, sched, r, it); ++r) {
             const int nk = it.nk(t), tok = it.tok0 + t * a.ntok + row_tok;
             const int lim = it.L - it.n + tok;              // last key that this row sees
+            const bool valid = row < a.ntok * a.G && tok < it.n;
             const int n = max(nk, it.nk(1 - t));
             float m = kNone;
             uint64_t sum = pair(0.0f, 0.0f);
@@ -632,12 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 t0 = max3(t0, s[60], s[61]);
                 t1 = max3(t1, s[62], s[63]);
-                const float top = fmaxf(max3(t0, t1, t2), t3) * a.c;
+                t0 = max3(t0, t1, t2);
+                // rows that are not stored take no part in what the warp decides together
+                const float top = valid ? max3(t0, t0, t3) * a.c : -INFINITY;
                 // the accumulator keeps its old maximum until the new one is 2^8 larger (the first tile counts as such);
-                // a warp rescales together
-                if (__any_sync(0xffffffffu, top > m + kLazy)) {
+                // a warp rescales together.  A NaN becomes the maximum, and with it every weight of its row
+                if (__any_sync(0xffffffffu, !(top <= m + kLazy))) {
                     const float was = m;
-                    m = top > m + kLazy ? top : m;
+                    m = top <= m + kLazy ? m : top;
                     const float f = ex2(was - m);
                     // the product before this step still adds to O
                     if (j > 0)
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nk > 0)
                 wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
             slot += 2 * n;
-            const bool store = ok && row < a.ntok * a.G && tok < it.n, sees = lim >= 0;
+            const bool store = ok && valid, sees = lim >= 0;
             const int head = it.kvh * a.G + row_head;
             const int64_t q_row = static_cast<int64_t>(it.q0) + tok;
             float l0, l1;

@@ -178,6 +178,52 @@ def test_prefill_growing_maximum():
     check_prefill(q, K, V, [0, n], lambda b: (K, V), out, lse)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_prefill_nan_keys_reach_the_rows_that_see_them(dtype):
+    # a NaN key at every place of a tile: rows before it as without it, rows from it on NaN
+    g = torch.Generator().manual_seed(21)
+    n, batch = 90, 70
+    q, K, V = (values(g, (n, h, 64), dtype).cuda() for h in (2, 1, 1))
+    clean, _ = prefill(q, K, V, [0, n])
+    bad = [1 + i for i in range(batch)]
+    K2 = K.repeat(batch, 1, 1)
+    for i, at in enumerate(bad):
+        K2[i * n + at, 0, 5] = math.nan
+    out, lse = prefill(q.repeat(batch, 1, 1), K2, V.repeat(batch, 1, 1), [n * i for i in range(batch + 1)])
+    for i, at in enumerate(bad):
+        rows, logs = out[i * n:(i + 1) * n], lse[i * n:(i + 1) * n]
+        assert torch.equal(rows[:at], clean[:at]), at
+        assert rows[at:].isnan().all() and logs[at:].isnan().all(), at
+
+
+def test_prefill_masked_values_of_the_types_limit():
+    # values of 2^127 that earlier rows do not see leave those rows as they were
+    g = torch.Generator().manual_seed(22)
+    n = 128
+    q, K, V = (values(g, (n, h, 128), torch.bfloat16).cuda() for h in (4, 1, 1))
+    clean, _ = prefill(q, K, V, [0, n])
+    for at in (1, 17, 63, 64, 100):
+        V2 = V.clone()
+        V2[at:] = 2.0 ** 127
+        out, _ = prefill(q, K, V2, [0, n])
+        assert torch.equal(out[:at], clean[:at]), at
+
+
+def test_prefill_logits_of_any_size():
+    # every logit near -2^110: the largest still gives its row a finite mean
+    n, d = 70, 64
+    q = torch.zeros((n, 1, d), dtype=torch.bfloat16, device="cuda")
+    K = torch.zeros((n, 1, d), dtype=torch.bfloat16, device="cuda")
+    V = values(torch.Generator().manual_seed(23), (n, 1, d), torch.bfloat16).cuda()
+    q[..., 0] = 2.0 ** 56
+    K[..., 0] = -(2.0 ** 57)
+    out, _ = prefill(q, K, V, [0, n])
+    want = V.double().cumsum(0) / torch.arange(1, n + 1, device="cuda")[:, None, None]
+    mag = V.double().abs().cumsum(0) / torch.arange(1, n + 1, device="cuda")[:, None, None]
+    # equal weights of exactly 2^0: one 32-bit addition per key, one division, the output's rounding
+    assert ((out.double() - want).abs() <= mag * (2 * n * 2.0 ** -23) + 2.0 ** -8 * want.abs()).all()
+
+
 def test_prefill_reports_bad_offsets_and_serves_the_rest():
     g = torch.Generator().manual_seed(10)
     q, K, V = (values(g, (200, h, 128), torch.bfloat16).cuda() for h in (4, 1, 1))
