@@ -436,18 +436,65 @@ def _take_error(status) -> int:
     return v
 
 
+def _torch_dtype(code: int):
+    import torch
+
+    return {RKV_DTYPE_BF16: torch.bfloat16, RKV_DTYPE_F32: torch.float32, RKV_DTYPE_F16: torch.float16}.get(code)
+
+
+def _need(where: str, name: str, x, n: int, dtype, strided=False):
+    """Refuses a tensor of another type, or with fewer than n elements to reach from its first one: those of a
+    contiguous tensor or, where the layout is described apart from it (strided), those of its storage."""
+    if x.dtype is dtype:
+        if x.is_contiguous():
+            if x.numel() >= n:
+                return
+        elif strided and x.untyped_storage().nbytes() // x.element_size() - x.storage_offset() >= n:
+            return
+    _refuse(where, f"{name} must be {dtype}" + ("" if strided else ", contiguous") + f" and hold {n} elements")
+
+
 class Prefill:
     """Causal attention over packed prompts: a configuration and its device status word."""
 
     def __init__(self, cfg: rkv_prefill_config, device="cuda"):
         import torch
 
-        self.cfg = cfg
+        c = self.cfg = rkv_prefill_config.from_buffer_copy(cfg)
+        self._in, self._out, self._i32, self._f32 = (_torch_dtype(c.in_dtype), _torch_dtype(c.out_dtype), torch.int32,
+                                                     torch.float32)
+
+        def reach(rows, row, heads, head, planes=1, plane=0):
+            return (rows - 1) * row + (heads - 1) * head + (planes - 1) * plane + c.head_dim if rows > 0 else 0
+
+        self._offs = (c.batch + 1, c.batch if c.kv_padded else c.batch + 1, c.batch, c.q_rows * c.n_q_heads)
+        self._q_reach = reach(c.q_rows, c.q_row_stride, c.n_q_heads, c.q_head_stride)
+        self._out_reach = reach(c.q_rows, c.out_row_stride, c.n_q_heads, c.out_head_stride)
+        self._kv_reach = reach(c.kv_rows, c.kv_row_stride, c.n_kv_heads, c.kv_head_stride,
+                               c.batch if c.kv_padded else 1, c.kv_plane_stride)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
     def attend(self, q, K, V, q_off, out, kv_off=None, kv_len=None, lse=None, stream=None):
-        """q_off, kv_off: int32 [batch + 1], kv_len: int32 [batch], all on the device; layouts as in
-        make_prefill_config."""
+        """q_off, kv_off: int32 [batch + 1], kv_len: int32 [batch], lse: float32 [q_rows, q_heads], all on the device;
+        q, K, V and out laid out as the configuration's strides say."""
+        dt, kv = self._in, self._kv_reach
+        if not (q.dtype is dt and K.dtype is dt and V.dtype is dt and out.dtype is self._out and q.is_contiguous() and
+                K.is_contiguous() and V.is_contiguous() and out.is_contiguous() and q.numel() >= self._q_reach and
+                K.numel() >= kv and V.numel() >= kv and out.numel() >= self._out_reach):
+            # strided views, or something to refuse
+            where = "Prefill.attend"
+            _need(where, "q", q, self._q_reach, dt, True)
+            _need(where, "K", K, kv, dt, True)
+            _need(where, "V", V, kv, dt, True)
+            _need(where, "out", out, self._out_reach, self._out, True)
+        n_off, n_kv_off, n_len, n_lse = self._offs
+        _need("Prefill.attend", "q_off", q_off, n_off, self._i32)
+        if kv_off is not None:
+            _need("Prefill.attend", "kv_off", kv_off, n_kv_off, self._i32)
+        if kv_len is not None:
+            _need("Prefill.attend", "kv_len", kv_len, n_len, self._i32)
+        if lse is not None:
+            _need("Prefill.attend", "lse", lse, n_lse, self._f32)
         rkv_prefill_attn(self.cfg, q, K, V, q_off, kv_off, kv_len, out, lse, self.status, stream)
 
     def device_error(self) -> int:
@@ -472,11 +519,14 @@ class BlockTables:
     def extend(self, new_counts, slot_map, stream=None):
         """Room for new_counts[b] more tokens of each request; their slots go to slot_map (int32, -1 behind the
         last), their packed offsets to new_off, and lengths grows."""
+        _need("BlockTables.extend", "new_counts", new_counts, self.cfg.batch, self.lengths.dtype)
+        _need("BlockTables.extend", "slot_map", slot_map, 0, self.lengths.dtype)
         rkv_blocks_extend(self.cfg, self.lengths, new_counts, self.table, self.free_list, self.n_free, self.new_off,
                           slot_map, slot_map.numel(), self.lengths, self.n_free, self.status, stream)
 
     def release(self, ended, stream=None):
-        """The blocks of the requests with a nonzero flag go back, their lengths become 0."""
+        """The blocks of the requests with a nonzero flag (int32) go back, their lengths become 0."""
+        _need("BlockTables.release", "ended", ended, self.cfg.batch, self.lengths.dtype)
         rkv_blocks_release(self.cfg, self.lengths, ended, self.table, self.free_list, self.n_free, self.lengths,
                            self.n_free, self.status, stream)
 
@@ -511,7 +561,13 @@ class KV8Cache:
         if workspace is None:
             workspace = torch.empty(max(256, self.ws_bytes), dtype=torch.uint8, device=device)
         self.workspace = workspace
-        _local("KV8Cache", (self.codes_K, self.codes_V, self.scale_K, self.scale_V, self.workspace))
+        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+            _refuse("KV8Cache", "workspace must be a contiguous torch.uint8 tensor")
+        _, self.device_index = _local("KV8Cache", (self.codes_K, self.codes_V, self.scale_K, self.scale_V, self.workspace,
+                                                   self.status))
+        self._in, self._out, self._i32 = _torch_dtype(cfg.in_dtype), _torch_dtype(cfg.out_dtype), torch.int32
+        self._row = (cfg.n_kv_heads, cfg.head_dim)
+        self._sizes = (cfg.batch * cfg.n_q_heads * cfg.head_dim, cfg.batch * cfg.max_blocks, cfg.batch)
         self.c = rkv_kv8_cache.from_buffer_copy(cfg)
         for name in ("codes_K", "codes_V", "scale_K", "scale_V"):
             setattr(self.c, name, getattr(self, name).data_ptr())
@@ -520,13 +576,34 @@ class KV8Cache:
     def store(self, K_new, V_new, slot_map, stream=None):
         """K_new, V_new: [rows, kv_heads, head_dim] with the same row and head strides and contiguous channels;
         slot_map: int32 [rows] (negative: the row is skipped)."""
-        if K_new.stride() != V_new.stride() or K_new.stride(2) != 1:
-            _refuse("KV8Cache.store", "K_new and V_new must have equal strides and contiguous channels")
-        rkv_kv8_store(self.c, K_new, V_new, K_new.stride(0), K_new.stride(1), slot_map, K_new.shape[0], stream)
+        where, shape, strides = "KV8Cache.store", K_new.shape, K_new.stride()
+        if len(shape) != 3 or shape[1:] != self._row or V_new.shape != shape or V_new.stride() != strides or \
+                strides[2] != 1 or K_new.dtype is not self._in or V_new.dtype is not self._in:
+            _refuse(where, f"K_new and V_new must be {self._in} [rows, {self._row[0]}, {self._row[1]}] with equal strides "
+                           "and contiguous channels")
+        _need(where, "slot_map", slot_map, shape[0], self._i32)
+        self._here(where)
+        rkv_kv8_store(self.c, K_new, V_new, strides[0], strides[1], slot_map, shape[0], stream)
 
     def decode(self, q, block_table, lengths, out, stream=None):
-        """q, out: [batch, q_heads, head_dim]; block_table: int32 [batch, max_blocks]; lengths: int32 [batch]."""
+        """q, out: [batch, q_heads, head_dim]; block_table: int32 [batch, max_blocks]; lengths: int32 [batch]; all
+        contiguous.  One workspace: calls on several streams must not overlap."""
+        n, n_table, n_len = self._sizes
+        if not (q.dtype is self._in and out.dtype is self._out and q.numel() >= n and out.numel() >= n and
+                q.is_contiguous() and out.is_contiguous()):
+            _need("KV8Cache.decode", "q", q, n, self._in)
+            _need("KV8Cache.decode", "out", out, n, self._out)
+        _need("KV8Cache.decode", "block_table", block_table, n_table, self._i32)
+        _need("KV8Cache.decode", "lengths", lengths, n_len, self._i32)
+        self._here("KV8Cache.decode")
         rkv_kv8_decode_attn(self.c, q, block_table, lengths, out, self.workspace, self.workspace.numel(), stream)
+
+    def _here(self, where):
+        """The cache's buffers go into calls as addresses: their device has to be the current one."""
+        import torch
+
+        if torch._C._cuda_getDevice() != self.device_index:
+            _refuse(where, f"the cache is on cuda:{self.device_index}, which is not the current device")
 
     def device_error(self) -> int:
         return _take_error(self.status)
