@@ -25,7 +25,9 @@
 //
 // Work split: items (sequence, pair of query tiles, kv-head), sequences sorted by their number of keys and pairs
 // from the last (most keys) to the first, taken in snake order by one persistent CTA per SM.  Everything is
-// derived from the offsets on the device, so a captured graph follows them.
+// derived from the offsets on the device, so a captured graph follows them.  Few items over many keys (the next
+// tokens of a long request) are split along the keys: the CTAs of a cluster each take a range of an item's key tiles
+// and join their parts through their shared memory (split_of says when), without a workspace.
 //
 // Warps: 0 TMA producer, 1 and 2 issue S of query tiles 0 and 1, 3 issues P V of both, 4-7 and 8-11 are their softmax.
 // Every wait is bounded (2 s); one that gives up records RKV_ERR_TIMEOUT, all roles leave their loops, and copies
@@ -35,6 +37,7 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "launchers.h"
@@ -245,6 +248,73 @@ __device__ __forceinline__ uint32_t pack2(float x, float y)
     }
 }
 
+// ---- clusters: barriers and shared memory of the other CTAs -----------------------------------
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(smem_addr(bar), rank))
+                 : "memory");
+}
+
+// mbar_wait for what the threads of other CTAs wrote before they arrived.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort)
+{
+    if (!mbar_wait(bar, parity, abort))
+        return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ float4 peer_float4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 peer_float2(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 // ---- work items ------------------------------------------------------------------------------
 
 // Rows and keys of a sequence; ok = false if they leave q or K.
@@ -334,10 +404,10 @@ struct Item {
     __device__ __forceinline__ int last_width(int t) const { return ((last_key(t) % kN) + 16) & ~15; }
 };
 
-// The r-th item of this CTA; false if there is none (with the snake order only the last round can lack one).
-__device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& sc, int r, Item& it)
+// The r-th item of worker p of P (CTAs or clusters); false if there is none (with the snake order only the last
+// round can lack one).
+__device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& sc, unsigned P, unsigned p, int r, Item& it)
 {
-    const unsigned P = gridDim.x, p = blockIdx.x;
     const unsigned total = static_cast<unsigned>(sc.pairs[a.batch]) * a.Hkv;
     const unsigned idx = r * P + ((r & 1) ? P - 1 - p : p);
     if (idx >= total)
@@ -364,6 +434,9 @@ __device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& s
     return true;
 }
 
+constexpr uint32_t kMaxParts = 8;       // CTAs that share an item's keys: the largest portable cluster
+constexpr int kJoinBar = 9;             // named barrier of the softmax warps (1 to 8: their turns)
+
 // Output staging of a softmax warp: 32 rows of 64 bytes.
 constexpr uint32_t kStage = 32 * 64;
 
@@ -379,13 +452,14 @@ template <int kStages>
 struct Bars {
     uint64_t q_full[2], q_empty[2], kv_full[kStages], kv_empty[kStages];
     uint64_t s_full[2], s_free[2], p_ready[2][2], pv_done[2][2], last[3];   // [query tile][P buffer]
+    uint64_t part_full, part_read;   // of a cluster: every CTA's part of an item is there; every CTA has read this one's
     uint32_t tmem;
     int abort;
     int issued;                 // ring slots filled so far (producer, at its end)
     int q_issued[2];
 };
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                    const __grid_constant__ CUtensorMap mV, const PrefillArgs a)
@@ -399,6 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Schedule sched;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &bars->abort;
+    const uint32_t parts = kSplit ? cluster_size() : 1, part = kSplit ? cluster_rank() : 0;
+    const unsigned workers = gridDim.x / parts, worker = blockIdx.x / parts;
+    auto item_at = [&](int r, Item& it) { return get_item(a, sched, workers, worker, r, it); };
+    // this CTA's key tiles of an item that needs n
+    auto first_tile = [&](int n) { return kSplit ? static_cast<int>(n * part / parts) : 0; };
+    auto end_tile = [&](int n) { return kSplit ? static_cast<int>(n * (part + 1) / parts) : n; };
 
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
@@ -419,6 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars->last[0], 1);
         mbar_init(&bars->last[1], 1);
         mbar_init(&bars->last[2], 1);
+        if constexpr (kSplit) {
+            mbar_init(&bars->part_full, parts + 1);              // the softmax warps of every CTA, and this one's producer
+            mbar_init(&bars->part_read, parts);
+        }
         bars->abort = 0;
         bars->issued = 0;
         fence_mbar_init();
@@ -433,6 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     make_schedule(a, sched);
     tc_fence_before();
     __syncthreads();
+    if constexpr (kSplit)
+        cluster_sync_all();                                      // the other CTAs' barriers are there
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     const uint32_t q_smem = smem_addr(sm + L::q), kv_smem = smem_addr(sm + L::kv);
@@ -469,13 +555,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 &bars->kv_full[st]);
                 ++slot;
             };
-            for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
-                const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (j == 0 && n0 > 0)
+            for (int r = 0; (ok || kSplit) && item_at(r, it); ++r) {
+                const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1), jb = first_tile(n), je = end_tile(n);
+                if constexpr (kSplit) {
+                    // the ring held this CTA's part of the item before.  Arriving here for every item, whatever
+                    // happened, keeps this thread within one phase of part_read
+                    if (r > 0)
+                        ok = ok && mbar_wait_sleep(&bars->part_read, (r - 1) & 1, abort);
+                    mbar_arrive(&bars->part_full);
+                }
+                for (int j = jb; ok && j < je; ++j) {
+                    if (j == jb && n0 > jb)
                         load_q(0, q_use0);
                     load_kv(&mK, j);
-                    if (j == 0 && n1 > 0)
+                    if (j == jb && n1 > jb)
                         load_q(1, q_use1);
                     load_kv(&mV, j);
                 }
@@ -503,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t q_desc = smem_desc_sw128(q_smem + t * L::qtile), k_desc = smem_desc_sw128(kv_smem);
                 const uint32_t tm_s = tmem + 128 * t;
                 uint32_t q_use = 0, c = 0;
-                for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
-                    const int nk = it.nk(t), n = max(nk, it.nk(1 - t));
-                    for (int j = 0; j < n; ++j, slot += 2) {
+                for (int r = 0; ok && item_at(r, it); ++r) {
+                    const int nk = it.nk(t), n = max(nk, it.nk(1 - t)), jb = first_tile(n), je = end_tile(n);
+                    for (int j = jb; j < je; ++j, slot += 2) {
                         const uint32_t ks = slot % kStages;
                         if (!wait(&bars->kv_full[ks], (slot / kStages) & 1))
                             break;
@@ -513,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_arrive(&bars->kv_empty[ks]);      // the other query tile's alone
                             continue;
                         }
-                        if (j == 0 && !wait(&bars->q_full[t], q_use++ & 1))
+                        if (j == jb && !wait(&bars->q_full[t], q_use++ & 1))
                             break;
                         // P V of step c - 2 has read the P buffer that follows from this S, and S of step c - 1 is in the
                         // softmax warps' registers
@@ -532,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     kd + (kk / 4) * ((kN * 128) >> 4) + (kk % 4) * 2, idesc, kk > 0 ? 1u : 0u);
                         mma_commit(&bars->s_full[t]);
                         mma_commit(&bars->kv_empty[ks]);
-                        if (j + 1 == nk)
+                        if (j + 1 == min(nk, je))
                             mma_commit(&bars->q_empty[t]);
                         ++c;
                     }
@@ -552,17 +645,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        vd + kk * (2048 >> 4), idescO, (first && kk == 0) ? 0u : 1u);
                     mma_commit(&bars->pv_done[t][c & 1]);
                 };
-                for (int r = 0; ok && get_item(a, sched, r, it); ++r) {
-                    const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1);
-                    for (int j = 0; j < n; ++j, slot += 2) {
+                for (int r = 0; ok && item_at(r, it); ++r) {
+                    const int n0 = it.nk(0), n1 = it.nk(1), n = max(n0, n1), jb = first_tile(n), je = end_tile(n);
+                    for (int j = jb; j < je; ++j, slot += 2) {
                         const uint32_t vs = (slot + 1) % kStages;
                         if (!wait(&bars->kv_full[vs], ((slot + 1) / kStages) & 1))
                             break;
                         const uint64_t vd = v_desc + vs * kTileDesc;
                         if (j < n0)
-                            issue_pv(0, c0++, vd, (j + 1 < n0 ? kN : it.last_width(0)) / 16, j == 0);
+                            issue_pv(0, c0++, vd, (j + 1 < n0 ? kN : it.last_width(0)) / 16, j == jb);
                         if (j < n1)
-                            issue_pv(1, c1++, vd, (j + 1 < n1 ? kN : it.last_width(1)) / 16, j == 0);
+                            issue_pv(1, c1++, vd, (j + 1 < n1 ? kN : it.last_width(1)) / 16, j == jb);
                         if (!ok)
                             break;
                         mma_commit(&bars->kv_empty[vs]);
@@ -599,14 +692,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t == 1)
             named_arrive(other_turn, 64);
         // after a wait gave up the loops go on without work, so that the turns stay matched
-        for (int r = 0; get_item(a, sched, r, it); ++r) {
+        for (int r = 0; item_at(r, it); ++r) {
             const int nk = it.nk(t), tok = it.tok0 + t * a.ntok + row_tok;
             const int lim = it.L - it.n + tok;              // last key that this row sees
             const bool valid = row < a.ntok * a.G && tok < it.n;
-            const int n = max(nk, it.nk(1 - t));
+            const int n = max(nk, it.nk(1 - t)), jb = first_tile(n), je = end_tile(n), jt = min(nk, je);
             float m = kNone;
             uint64_t sum = pair(0.0f, 0.0f);
-            for (int j = 0; j < nk; ++j, ++c) {
+            for (int j = jb; j < jt; ++j, ++c) {
                 wait(&bars->s_full[t], c & 1);
                 float s[64];
                 tmem_ld32_async(tm_s, s);
@@ -645,13 +738,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = top <= m + kLazy ? m : top;
                     const float f = ex2(was - m);
                     // the product before this step still adds to O
-                    if (j > 0)
+                    if (j > jb)
                         wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
                     float x0, x1;
                     unpair(sum, x0, x1);
                     sum = pair(x0 * f, x1 * f);
 #pragma unroll 1
-                    for (int x = 0; j > 0 && x < D / 16; ++x) {
+                    for (int x = 0; j > jb && x < D / 16; ++x) {
                         uint32_t w[16];
                         float o[16];
                         tmem_ld16(tm_o + 16 * x, o);
@@ -664,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j == n - 1 && (it.L & 15) && n * kN > it.L) {
                     // V rows behind the last key, within its group of 16, meet weights of 0 in the product: they may
                     // hold NaN and are zeroed, by the warps of each query tile before they hand over P
-                    const uint32_t vs = slot + 2 * j + 1;
+                    const uint32_t vs = slot + 2 * (j - jb) + 1;
                     wait(&bars->kv_full[vs % kStages], (vs / kStages) & 1);
                     const int left = it.L - j * kN;
                     for (int i = row; ok && i < (16 - (left & 15)) * kHalves * 8; i += 128) {
@@ -709,19 +802,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars->p_ready[t][c & 1]);
                 sum = add2(sum, add2(a0, a1));
             }
-            for (int j = nk; j < n; ++j) {                  // steps of the other query tile alone
+            for (int j = max(jt, jb); j < je; ++j) {        // steps of the other query tile alone
                 named_sync(my_turn, 64);
                 named_arrive(other_turn, 64);
             }
-            if (nk > 0)
+            if (jt > jb)
                 wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
-            slot += 2 * n;
+            slot += 2 * (je - jb);
             const bool store = ok && valid, sees = lim >= 0;
             const int head = it.kvh * a.G + row_head;
             const int64_t q_row = static_cast<int64_t>(it.q0) + tok;
             float l0, l1;
             unpair(sum, l0, l1);
-            const float l = l0 + l1, inv = sees ? 1.0f / l : 0.0f;
+            const float l = l0 + l1;
+            if constexpr (kSplit) {
+                // The parts (m, l, O) of the cluster's CTAs go through the ring, which the item has left, and CTA `part` joins
+                // the columns from part * D / parts on: M = max m_x, f_x = 2^(m_x - M), O = sum f_x O_x / sum f_x l_x.
+                // Parts without a key tile are (lowest float, 0, 0).
+                if (r > 0)
+                    wait(&bars->part_read, (r - 1) & 1);
+                named_sync(kJoinBar, 256);                       // the products of both query tiles are done
+                const uint32_t ml_at = L::stage + (t * kM + row) * 8, o_at = L::kv + t * (kM * D * 4) + row * 16;
+                *reinterpret_cast<float2*>(sm + ml_at) = make_float2(m, l);
+#pragma unroll 1
+                for (int x = 0; x < D / 32; ++x) {
+                    float o[32];
+                    tmem_ld32(tm_o + 32 * x, o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4*>(sm + o_at + (8 * x + i) * (kM * 16)) =
+                            jt > jb ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                tc_fence_before();                               // the next item's first product overwrites O
+                fence_proxy_async_smem();                        // later copies into the ring come after these stores
+                named_sync(kJoinBar, 256);
+                if (warp == 4 && lane < parts)
+                    arrive_at(&bars->part_full, lane);
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, ok && mbar_wait_cluster(&bars->part_full, r & 1, abort));
+                // all of a thread's loads from the other CTAs are under way at once
+                float2 ml[kMaxParts];
+#pragma unroll
+                for (uint32_t x = 0; x < kMaxParts; ++x)
+                    ml[x] = x < parts ? peer_float2(peer_addr(smem_addr(sm + ml_at), x)) : make_float2(kNone, 0.0f);
+                float M = kNone, sum_l = 0.0f;
+#pragma unroll
+                for (uint32_t x = 0; x < kMaxParts; ++x)
+                    M = max3(M, M, ml[x].x);
+#pragma unroll
+                for (uint32_t x = 0; x < kMaxParts; ++x) {
+                    ml[x].x = ex2(ml[x].x - M);
+                    sum_l = fmaf(ml[x].x, ml[x].y, sum_l);
+                }
+                const float inv = sees ? 1.0f / sum_l : 0.0f;
+                if (store && a.lse && part == 0)
+                    a.lse[q_row * a.Hq + head] = sees ? (M - kBias<kF16> + log2f(sum_l)) * 0.6931471805599453f : -INFINITY;
+                const int cols = D / static_cast<int>(parts);
+#pragma unroll 1
+                for (int col = part * cols; col < static_cast<int>(part + 1) * cols; col += 8) {
+                    float4 v[kMaxParts][2];
+#pragma unroll
+                    for (uint32_t x = 0; x < kMaxParts; ++x)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            v[x][h] = x < parts ? peer_float4(peer_addr(smem_addr(sm + o_at + (col / 4 + h) * (kM * 16)), x))
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float o[8] = {};
+#pragma unroll
+                    for (uint32_t x = 0; x < kMaxParts; ++x)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            o[4 * h] = fmaf(ml[x].x, v[x][h].x, o[4 * h]);
+                            o[4 * h + 1] = fmaf(ml[x].x, v[x][h].y, o[4 * h + 1]);
+                            o[4 * h + 2] = fmaf(ml[x].x, v[x][h].z, o[4 * h + 2]);
+                            o[4 * h + 3] = fmaf(ml[x].x, v[x][h].w, o[4 * h + 3]);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = sees ? o[i] * inv : 0.0f;
+                    if (!store)
+                        continue;
+                    const int64_t at = q_row * a.out_row_stride + head * a.out_head_stride + col;
+                    if (a.out_dtype == RKV_DTYPE_F32) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+                        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                    } else {
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) =
+                            make_uint4(pack2<kF16>(o[0], o[1]), pack2<kF16>(o[2], o[3]), pack2<kF16>(o[4], o[5]),
+                                       pack2<kF16>(o[6], o[7]));
+                    }
+                }
+                named_sync(kJoinBar, 256);
+                if (warp == 4 && lane < parts)
+                    arrive_at(&bars->part_read, lane);
+                __syncwarp();
+                continue;
+            }
+            const float inv = sees ? 1.0f / l : 0.0f;
             if (store && a.lse)
                 a.lse[q_row * a.Hq + head] = sees ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
             // Rows go out through a small staging area of the warp, 64 bytes of each at a time, so that four lanes store
@@ -792,6 +971,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    if constexpr (kSplit) {
+        __syncwarp();
+        cluster_sync_all();                                      // no CTA leaves while others may read its shared memory
+    }
 }
 
 using EncodeFn = PFN_cuTensorMapEncodeTiled_v12000;
@@ -820,16 +1003,43 @@ bool make_map(CUtensorMap* m, const void* base, bool f16, int rank, const cuuint
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kF16>
+template <int D, bool kF16, bool kSplit>
 cudaError_t launch_t(const CUtensorMap& mQ, const CUtensorMap& mK, const CUtensorMap& mV, const PrefillArgs& a,
-                     int ctas, cudaStream_t st)
+                     int workers, int parts, cudaStream_t st)
 {
-    auto kern = prefill_kernel<D, kF16>;
+    auto kern = prefill_kernel<D, kF16, kSplit>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::alloc);
     if (e != cudaSuccess)
         return e;
-    kern<<<ctas, kThreads, Layout<D>::alloc, st>>>(mQ, mK, mV, a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(workers * parts);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Layout<D>::alloc;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kSplit ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, mQ, mK, mV, a);
+}
+
+// CTAs that share the keys of an item, as a cluster.  The join costs about as much as 9 key tiles, and a second round
+// of items more than a split saves, so: the most CTAs that still run all at once (a GPU Processing Cluster holds
+// whole clusters only: 16 clusters of eight CTAs need two rounds, 12 do not, so eight must fit three quarters of the
+// SMs) and take at least 10 tiles off a sequence of mean length.  Measured for new tokens over earlier keys, 1 / 2 / 4 / 8
+// CTAs: 4 items of 100000 keys (head_dim 64) 903 / 454 / 238 / 127 us; 8 items of 1200 17.1 / 17.0 / 14.9 / 13.9 us, of
+// 600 12.6 / 14.4 / 13.2 / 12.7 us; 16 items of 2400 28.3 / 22.4 / 18.0 / 28.4 us; 64 items of 1000 24.6 / 23.1 / 45.4 us.
+int split_of(int64_t items, const rkv_prefill_config& c, int sms)
+{
+    const int64_t tiles = c.kv_rows / kN / (c.kv_padded ? 1 : c.batch);
+    int parts = 1;
+    for (int p = 2; p <= static_cast<int>(kMaxParts); p *= 2)
+        if (items * p <= (p == 8 ? sms * 3 / 4 : sms) && tiles - tiles / p >= 10)
+            parts = p;
+    return parts;
 }
 
 }  // namespace
@@ -881,10 +1091,19 @@ cudaError_t launch_prefill(const rkv_prefill_config& c, const void* q, const voi
     const int64_t items = (c.q_rows / (2 * a.ntok) + c.batch) * c.n_kv_heads;
     if (items > INT32_MAX)
         return cudaErrorInvalidValue;
-    const int ctas = static_cast<int>(items < sms ? items : sms);
+    const int parts = split_of(items, c, sms);
+    const int workers = static_cast<int>(items < sms / parts ? items : sms / parts);
+    auto launch = [&](auto d, auto half) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool kF16 = decltype(half)::value;
+        return parts > 1 ? launch_t<D, kF16, true>(mQ, mK, mV, a, workers, parts, st)
+                         : launch_t<D, kF16, false>(mQ, mK, mV, a, workers, 1, st);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
     if (c.head_dim == 128)
-        return f16 ? launch_t<128, true>(mQ, mK, mV, a, ctas, st) : launch_t<128, false>(mQ, mK, mV, a, ctas, st);
-    return f16 ? launch_t<64, true>(mQ, mK, mV, a, ctas, st) : launch_t<64, false>(mQ, mK, mV, a, ctas, st);
+        return f16 ? launch(D128{}, std::true_type{}) : launch(D128{}, std::false_type{});
+    return f16 ? launch(D64{}, std::true_type{}) : launch(D64{}, std::false_type{});
 }
 
 }  // namespace rkv

@@ -112,6 +112,53 @@ def test_prefill_chunks_over_earlier_keys(d):
     assert (out[qo[4]:qo[5]] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,out_dtype", [(torch.bfloat16, None), (torch.float16, None), (torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("hq,hkv,d,keys,new", [
+    # few items over many keys (shared by 8, 4 and 2 CTAs); one, all or no key tile for some of them
+    (8, 1, 128, [5000], [1]), (8, 1, 64, [1300], [37]), (7, 1, 128, [4000, 3, 900], [5, 3, 40]),
+    (4, 2, 64, [2500, 0, 64, 63], [1, 2, 70, 1]), (16, 8, 128, [1500, 1601], [1, 16]), (32, 8, 64, [1700] * 4, [1, 9, 17, 0]),
+    (24, 8, 128, [2600, 1300, 65, 700], [40, 1, 65, 50]), (2, 2, 128, [1025], [1025]),
+])
+def test_prefill_keys_shared_by_a_cluster(dtype, out_dtype, hq, hkv, d, keys, new):
+    g = torch.Generator().manual_seed(hq + d + len(keys))
+    q = values(g, (sum(new), hq, d), dtype).cuda()
+    # gaps of 5 rows between the sequences' keys, which hold NaN
+    K, V = (values(g, (sum(keys) + 5 * len(keys), hkv, d), dtype).cuda() for _ in range(2))
+    starts = [o + 5 * i for i, o in enumerate(offsets(keys)[:-1])]
+    for s, n in zip(starts, keys):
+        K[s + n:s + n + 5] = math.nan
+        V[s + n:s + n + 5] = math.nan
+    off = offsets(new)
+    kw = {} if out_dtype is None else dict(out_dtype=CODE[out_dtype])
+    first = None
+    for _ in range(3):
+        out, lse = prefill(q, K, V, off, kw, kv_off=starts + [0], kv_len=keys)
+        check_prefill(q, K, V, off, lambda b: (K[starts[b]:starts[b] + keys[b]], V[starts[b]:starts[b] + keys[b]]), out, lse)
+        first = first or (out, lse)
+        assert torch.equal(first[0], out) and torch.equal(first[1], lse)
+
+
+def test_prefill_split_calls_on_two_streams():
+    # two long single-token calls at once, repeated: no state is shared
+    g = torch.Generator().manual_seed(31)
+    jobs = []
+    for i in range(2):
+        q, K, V = (values(g, (n, h, 128), torch.bfloat16).cuda() for n, h in ((2, 8), (9000, 1), (9000, 1)))
+        op = rkv.Prefill(rkv.make_prefill_config(128, 1, 8, 1, 2, 9000))
+        want = torch.empty_like(q)
+        op.attend(q, K, V, ints([0, 2]), want, kv_off=ints([0, 9000]))
+        jobs.append((op, q, K, V, ints([0, 2]), ints([0, 9000]), want, torch.cuda.Stream(), [torch.empty_like(q) for _ in range(30)]))
+    torch.cuda.synchronize()
+    for r in range(30):
+        for op, q, K, V, qo, ko, want, st, outs in jobs:
+            with torch.cuda.stream(st):
+                op.attend(q, K, V, qo, outs[r], kv_off=ko)
+    torch.cuda.synchronize()
+    for op, q, K, V, qo, ko, want, st, outs in jobs:
+        assert op.device_error() == 0
+        assert all(torch.equal(o, want) for o in outs)
+
+
 def test_prefill_padded_planes_of_the_compressor_layout():
     # K, V [batch][kv_heads][max_len][d] with lengths shorter than the planes; rows behind the lengths hold NaN
     g = torch.Generator().manual_seed(6)
