@@ -306,27 +306,32 @@ def _refuse(where: str, why: str):
     raise RkvError(STATUS_CODE["RKV_ERR_INVALID_ARG"], f"{where} ({why})")
 
 
+_device = _raw = None          # torch's current device and its current stream as an address, once torch is there
+
+
+def _torch_calls():
+    global _device, _raw
+    import torch
+
+    _device, _raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(where, x, cur):
+    _refuse(where, f"a tensor on {x.device}, not on cuda:{cur}")
+
+
 def _local(where: str, tensors):
     """Device addresses of tensors (None and plain addresses pass) and the current device's ordinal; tensors of
     another device, whose streams the call would not follow, are refused."""
-    import torch
-
-    cur = torch._C._cuda_getDevice()
-    out = []
-    for x in tensors:
-        if isinstance(x, torch.Tensor):
-            if x.get_device() != cur:
-                _refuse(where, f"a tensor on {x.device}, not on cuda:{cur}")
-            out.append(x.data_ptr())
-        else:
-            out.append(x)
-    return out, cur
+    if _device is None:
+        _torch_calls()
+    cur = _device()
+    return [x if x is None or x.__class__ is int else x.data_ptr() if x.get_device() == cur else _elsewhere(where, x, cur)
+            for x in tensors], cur
 
 
 def _raw_stream(stream, cur: int) -> int:
-    import torch
-
-    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else _stream(stream)
+    return _raw(cur) if stream is None else _stream(stream)
 
 
 def rkv_prefill_attn(cfg: rkv_prefill_config, q, K, V, q_off, kv_off, kv_len, out, lse, device_status, stream=None):
@@ -600,9 +605,7 @@ class KV8Cache:
 
     def _here(self, where):
         """The cache's buffers go into calls as addresses: their device has to be the current one."""
-        import torch
-
-        if torch._C._cuda_getDevice() != self.device_index:
+        if _device() != self.device_index:
             _refuse(where, f"the cache is on cuda:{self.device_index}, which is not the current device")
 
     def device_error(self) -> int:

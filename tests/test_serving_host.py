@@ -203,7 +203,7 @@ def recorded(monkeypatch):
     for name in ("rkv_prefill_attn", "rkv_blocks_extend", "rkv_blocks_release", "rkv_kv8_store", "rkv_kv8_decode_attn"):
         monkeypatch.setattr(rkv, name, lambda *a, _n=name: calls.append((_n, a)))
     monkeypatch.setattr(rkv, "_local", lambda where, tensors: ([], 0))
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(rkv, "_device", lambda: 0)
     return calls
 
 
@@ -273,13 +273,13 @@ def test_cache_class_refuses_buffers_and_tensors(recorded, monkeypatch):
               (q, table, lens[:1], q), (q, table, lens, q.float()), (q, table, lens, q[:, :2])):
         refused(cache.decode, *a)
     assert len(recorded) == 2
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)      # another current device than the cache's
+    monkeypatch.setattr(rkv, "_device", lambda: 1)      # another current device than the cache's
     refused(cache.store, K, K, slots)
     refused(cache.decode, q, table, lens, q)
 
 
 def test_raw_calls_refuse_tensors_of_another_device(monkeypatch):
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(rkv, "_device", lambda: 0)
     x = torch.zeros(4, dtype=torch.int32)                            # on the CPU
     cfg = rkv.make_blocks_config(4, 2, 16, 8)
     with pytest.raises(rkv.RkvError) as e:
