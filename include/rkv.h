@@ -555,7 +555,7 @@ RKV_API rkv_status rkv_blocks_release(const rkv_blocks_config* cfg, const int32_
  * The uncompressed-reference alternative to the residual cache for pooled serving (no counterpart on the
  * pages).  Buffers are the caller's:
  *   codes_K, codes_V  [n_blocks][n_kv_heads][block_size][head_dim] bytes, 16-byte aligned
- *   scale_K, scale_V  [n_blocks][n_kv_heads] float
+ *   scale_K, scale_V  [n_blocks][n_kv_heads] float, 0 or at least 2^-64 in blocks that hold tokens
  *   device_status     device int32, zeroed by the caller before the first use
  *   code_type    RKV_KV8_INT8: codes -127..127; RKV_KV8_E4M3: 8-bit floats, 4 exponent and 3 mantissa
  *                bits, largest 448.  qmax is 127 or 448

@@ -52,7 +52,7 @@ rkv_status check_heads(int32_t head_dim, int32_t n_kv_heads, int32_t n_q_heads, 
     if (n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads != 0 || batch <= 0)
         return RKV_ERR_INVALID_ARG;
     if ((head_dim != 64 && head_dim != 128) || n_q_heads / n_kv_heads > 16 || batch > RKV_MAX_BATCH ||
-        n_kv_heads > 4096)
+        n_kv_heads > 4096 || n_q_heads > 65535)
         return RKV_ERR_UNSUPPORTED;
     return RKV_OK;
 }

@@ -49,7 +49,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;     // tokens per CTA step
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCtas = 160 * kCtasPerSm;
-constexpr float kNone = -1e30f;        // running maximum before any token
+constexpr float kNone = -FLT_MAX;      // running maximum before any token
 constexpr float kWeightExp = 15.0f;    // weights are kept times 2^15: binary16 then holds 2^-39 .. 1 of the largest
 
 struct DecodeArgs {
@@ -295,20 +295,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             float f[kSteps * 4];
             float top = 0.0f;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
+            for (int c = 0; c < D / 32; ++c) {               // channels 64 (c / 2) + 16 t + 8 (c % 2) .. + 7
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (head < a.G)
+                    x = __ldg(reinterpret_cast<const uint4*>(qu + head * D + 64 * (c / 2) + 16 * t + 8 * (c % 2)));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int ch = 64 * c + 16 * t + e;
-                    float v = 0.0f;
-                    if (head < a.G) {
-                        if constexpr (kF16)
-                            v = __half2float(__ushort_as_half(qu[head * D + ch]));
-                        else
-                            v = bf16_bits_to_f32(qu[head * D + ch]);
-                    }
-                    f[16 * c + e] = v;
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t u = e % 2 ? w[e / 2] >> 16 : w[e / 2] & 0xffffu;
+                    float v;
+                    if constexpr (kF16)
+                        v = __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+                    else
+                        v = bf16_bits_to_f32(u);
+                    f[8 * c + e] = v;
                     top = fmaxf(top, fabsf(v));
                 }
+            }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // q times 2^(15 - e): the largest element in [2^14, 2^15)
@@ -356,11 +359,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             next_id = block_id(ti + 2);
             const int next_row = (tok + kTile) & tok_mask;
 
-            // rows of the block past the request's end may hold anything, NaN codes too
-            if (tok + 16 > len || !live) {
+            // rows of the block past the request's end may hold anything, NaN codes too; a scale of 0 makes values of 0
+            const bool sv_ok = c.sv > 0.0f;
+            if (tok + 16 > len || !live || !sv_ok) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (!live || tok + 2 * t + (r & 1) + 8 * (r >> 1) >= len)
+                    if (!live || !sv_ok || tok + 2 * t + (r & 1) + 8 * (r >> 1) >= len)
                         c.v[r].zero();
             }
 
@@ -383,7 +387,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             const float sk = c.sk, sv = c.sv;
             c.load_k(a, id, next_row, kvh, lane);
             const bool in0 = live && tok + g < len, in1 = live && tok + g + 8 < len;
-            const bool sv_ok = sv > 0.0f;
             const float lsv = sv_ok ? __log2f(sv) : 0.0f, rsv = sv_ok ? __frcp_rn(sv) : 1.0f;
             uint32_t wf[NT][2];
 #pragma unroll
@@ -488,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             }
             if (whole) {
                 store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
-                          L > 0.0f ? O / L : 0.0f);
+                          L != 0.0f ? O / L : 0.0f);
             } else {
                 a.part_o[(part + head) * D + ch] = O;
                 if (ch == 0)
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, 
         for (int r = 0; r < kRows; ++r)
             v += reinterpret_cast<const float*>(s_o[r])[tid];
         store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + tid,
-                  L > 0.0f ? v / L : 0.0f);
+                  L != 0.0f ? v / L : 0.0f);
     }
 }
 

@@ -592,6 +592,102 @@ def test_decode_many_requests_and_sharp_queries():
     check_decode(cache, table, lens, q, out)
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_decode_zero_scales_and_nan_queries(code):
+    # a value scale of 0 makes its block's values 0 whatever the codes; a NaN in a query reaches its head alone
+    g = torch.Generator().manual_seed(9)
+    lens = [300, 5000]
+    cache, table = random_cache(g, code, lens, 64, 2, 6, 16, torch.bfloat16)
+    for b, j in ((0, 2), (0, 18), (1, 100)):
+        cache.scale_V[int(table[b, j])] = 0.0
+    q = values(g, (2, 6, 64), torch.bfloat16).cuda()
+    out = torch.empty_like(q)
+    cache.decode(q, table.cuda(), ints(lens), out)
+    assert cache.device_error() == 0
+    # rows behind the lengths hold NaN patterns: a reference block of zeros stands for scale 0
+    for b, j in ((0, 2), (0, 18), (1, 100)):
+        cache.codes_V[int(table[b, j])] = torch.zeros_like(cache.codes_V[0])
+    check_decode(cache, table, lens, q, out)
+    q2 = q.clone()
+    q2[0, 4, 63] = math.nan
+    q2[1, 0, 0] = math.nan
+    out2 = torch.empty_like(q)
+    cache.decode(q2, table.cuda(), ints(lens), out2)
+    hit = torch.zeros((2, 6), dtype=torch.bool)
+    hit[0, 4] = hit[1, 0] = True
+    assert out2[hit].isnan().all() and torch.equal(out2[~hit], out[~hit])
+
+
+def test_decode_logits_of_any_size():
+    # every logit near -2^111: the mean of the values all the same
+    cache, table = random_cache(torch.Generator().manual_seed(10), "int8", [200], 64, 1, 1, 16, torch.bfloat16, spread=0.0)
+    cache.codes_K.fill_(0)
+    cache.codes_K[..., 0] = -64
+    cache.scale_K.fill_(2.0 ** 52)
+    q = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0 ** 56
+    out = torch.empty((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    cache.decode(q, table.cuda(), ints([200]), out)
+    v = side_rows(cache.codes_V, cache.scale_V, table[0, :13].long(), 200)
+    want, mag = v.mean(0), v.abs().mean(0)
+    # equal logits x: log2 sV is added to x, whose step hides it, so the weights are equal before the V scales, which are
+    # all 2^0 / 30; a weight of 2^15, one 32-bit addition per token, the factors' roundings, the output's
+    assert ((out[0].double().cpu() - want).abs() <= mag * (2 * 200 + 8) * 2.0 ** -23 + 2.0 ** -8 * want.abs()).all()
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_cache_offsets_past_32_bits(code):
+    # 8.6 GB of codes a side: blocks at both ends of the pool
+    g = torch.Generator().manual_seed(11)
+    d, hkv, block, n_blocks = 128, 8, 128, 1 << 16
+    cache = cache_of(code, d=d, hkv=hkv, hq=hkv, block=block, n_blocks=n_blocks, max_blocks=3, batch=2)
+    table = torch.tensor([[n_blocks - 1, 0, n_blocks // 2 + 1], [n_blocks - 2, 1, 5]], dtype=torch.int32)
+    lens = [300, 130]
+    K, V = (values(g, (sum(lens), hkv, d), torch.bfloat16) for _ in range(2))
+    slots = [int(table[b, p // block]) * block + p % block for b, n in enumerate(lens) for p in range(n)]
+    cache.store(K.cuda(), V.cuda(), ints(slots))
+    small = table.flatten().tolist()                  # the same blocks in a pool of six
+    rk, rv = (ref.Store(6, hkv, block, d, code) for _ in range(2))
+    moved = [small.index(s // block) * block + s % block for s in slots]
+    rk.put(K, moved)
+    rv.put(V, moved)
+    ids = table.flatten().long().cuda()
+    for c, s, r in ((cache.codes_K, cache.scale_K, rk), (cache.codes_V, cache.scale_V, rv)):
+        assert torch.equal(s[ids].cpu(), r.scale)
+        assert torch.equal(c[ids].cpu().view(torch.uint8), r.codes.view(torch.uint8))
+    q = values(g, (2, hkv, d), torch.bfloat16).cuda()
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    cache.decode(q, table.cuda(), ints(lens), out)
+    near = rkv.KV8Cache(rkv.make_kv8_config(d, hkv, hkv, block, 6, 3, 2, KV8[code]), *(x[ids].contiguous() for x in (
+        cache.codes_K, cache.codes_V, cache.scale_K, cache.scale_V)))
+    near.decode(q, ints(range(6)).view(2, 3), ints(lens), want)
+    assert cache.device_error() == 0 and near.device_error() == 0
+    assert torch.equal(out, want)
+
+
+def test_prefill_offsets_past_32_bits():
+    # rows 2^24 elements apart in 10 GB: the last keys and outputs lie past 2^32 elements
+    g = torch.Generator().manual_seed(12)
+    n, step, d = 300, 1 << 24, 64
+    store = torch.empty(n * step, dtype=torch.bfloat16, device="cuda")
+    at = lambda k: torch.as_strided(store, (n, 2, d), (step, d, 1), 1024 * k)  # noqa: E731
+    q, K, V = (values(g, (n, 2, d), torch.bfloat16).cuda() for _ in range(3))
+    want, wlse = prefill(q, K, V, [0, 100, n])
+    for k, x in enumerate((q, K, V)):
+        at(k).copy_(x)
+    out, lse = prefill(at(0), at(1), at(2), [0, 100, n], dict(q_strides=(step, d), kv_strides=(step, d, 0),
+                                                              out_strides=(step, d)), out=at(3))
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+def test_prefill_without_keys():
+    # no key row at all: zeros and log-sums of -inf
+    q = torch.ones((5, 4, 64), dtype=torch.float16, device="cuda")
+    K = torch.empty((0, 2, 64), dtype=torch.float16, device="cuda")
+    out, lse = prefill(q, K, K, [0, 2, 5], kv_off=[0, 0, 0])
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
 def test_decode_reports_corruption():
     g = torch.Generator().manual_seed(3)
     lens = [100, 90]

@@ -45,6 +45,7 @@ def prefill_status(cfg, **kw):
     (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED), (dict(head_dim=0), UNSUPPORTED),
     (dict(n_kv_heads=0), INVALID), (dict(n_q_heads=0), INVALID), (dict(n_q_heads=7), INVALID),
     (dict(n_q_heads=34), UNSUPPORTED), (dict(n_kv_heads=4097, n_q_heads=4097), UNSUPPORTED),
+    (dict(n_kv_heads=4096, n_q_heads=65536), UNSUPPORTED),
     (dict(batch=0), INVALID), (dict(batch=257), UNSUPPORTED), (dict(in_dtype=rkv.RKV_DTYPE_F32), UNSUPPORTED),
     (dict(in_dtype=7), INVALID), (dict(out_dtype=rkv.RKV_DTYPE_F16), INVALID), (dict(out_dtype=-1), INVALID),
     (dict(scale=-1.0), INVALID), (dict(scale=math.inf), INVALID), (dict(scale=math.nan), INVALID),
@@ -150,8 +151,8 @@ def size_status(cfg):
 @pytest.mark.parametrize("call", [store_status, decode_status, size_status])
 @pytest.mark.parametrize("kw,code", [
     (dict(head_dim=80), UNSUPPORTED), (dict(n_kv_heads=0), INVALID), (dict(n_q_heads=9), INVALID),
-    (dict(n_q_heads=34), UNSUPPORTED), (dict(batch=0), INVALID), (dict(batch=257), UNSUPPORTED),
-    (dict(block_size=48), UNSUPPORTED), (dict(n_blocks=0), INVALID), (dict(max_blocks=-1), INVALID),
+    (dict(n_q_heads=34), UNSUPPORTED), (dict(n_kv_heads=4096, n_q_heads=65536), UNSUPPORTED),
+    (dict(batch=0), INVALID), (dict(batch=257), UNSUPPORTED), (dict(block_size=48), UNSUPPORTED), (dict(n_blocks=0), INVALID), (dict(max_blocks=-1), INVALID),
     (dict(n_blocks=2 ** 27), UNSUPPORTED), (dict(max_blocks=2 ** 27), UNSUPPORTED), (dict(code_type=2), INVALID),
     (dict(code_type=-1), INVALID), (dict(in_dtype=rkv.RKV_DTYPE_F32), UNSUPPORTED), (dict(in_dtype=5), INVALID),
     (dict(out_dtype=rkv.RKV_DTYPE_F16), INVALID), (dict(scale=-0.5), INVALID), (dict(scale=math.nan), INVALID),
