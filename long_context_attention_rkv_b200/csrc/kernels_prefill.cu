@@ -344,6 +344,8 @@ __device__ __forceinline__ Seq sequence(const PrefillArgs& a, int b)
     return s;
 }
 
+static_assert(RKV_MAX_BATCH <= kThreads - 32, "make_schedule and the barriers' set-up use other warps");
+
 struct Schedule {
     Seq seq[RKV_MAX_BATCH];
     int key[RKV_MAX_BATCH];             // keys of sequence b, for the order
@@ -367,6 +369,7 @@ __device__ __forceinline__ void make_schedule(const PrefillArgs& a, Schedule& s)
     __syncthreads();
     if (tid < a.batch) {
         int rank = 0;
+#pragma unroll 8
         for (int b = 0; b < a.batch; ++b)
             rank += s.key[b] > q.L || (s.key[b] == q.L && b < tid);
         s.order[rank] = tid;
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto first_tile = [&](int n) { return kSplit ? static_cast<int>(n * part / parts) : 0; };
     auto end_tile = [&](int n) { return kSplit ? static_cast<int>(n * (part + 1) / parts) : n; };
 
-    if (tid == 0) {
+    if (tid == kThreads - 1) {                                   // make_schedule leaves the last warps idle at first
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->q_full[t], 1);
             mbar_init(&bars->q_empty[t], 1);
@@ -683,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int my_turn = 1 + 2 * (warp & 3) + t, other_turn = 1 + 2 * (warp & 3) + 1 - t;
         uint32_t c = 0, slot = 0;                           // steps of this query tile, ring slots
         bool ok = true;
-        Item it;
+        Item it, next;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool got = ok && mbar_wait(bar, parity, abort);
             ok = __all_sync(0xffffffffu, got);
@@ -692,7 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t == 1)
             named_arrive(other_turn, 64);
         // after a wait gave up the loops go on without work, so that the turns stay matched
-        for (int r = 0; item_at(r, it); ++r) {
+        bool more = item_at(0, it);
+        for (int r = 0; more; ++r, it = next) {
             const int nk = it.nk(t), tok = it.tok0 + t * a.ntok + row_tok;
             const int lim = it.L - it.n + tok;              // last key that this row sees
             const bool valid = row < a.ntok * a.G && tok < it.n;
@@ -806,15 +810,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 named_sync(my_turn, 64);
                 named_arrive(other_turn, 64);
             }
-            if (jt > jb)
-                wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
+            // while the last product runs: the next item, and what the rows of this one need
             slot += 2 * (je - jb);
-            const bool store = ok && valid, sees = lim >= 0;
+            more = item_at(r + 1, next);
+            const bool sees = lim >= 0;
             const int head = it.kvh * a.G + row_head;
             const int64_t q_row = static_cast<int64_t>(it.q0) + tok;
+            const int64_t row_at = q_row * a.out_row_stride + head * a.out_head_stride;   // elements
             float l0, l1;
             unpair(sum, l0, l1);
-            const float l = l0 + l1;
+            const float l = l0 + l1, inv_l = sees ? 1.0f / l : 0.0f;
+            const float log_sum = sees ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            if (jt > jb)
+                wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
+            const bool store = ok && valid;
             if constexpr (kSplit) {
                 // The parts (m, l, O) of the cluster's CTAs go through the ring, which the item has left, and CTA `part` joins
                 // the columns from part * D / parts on: M = max m_x, f_x = 2^(m_x - M), O = sum f_x O_x / sum f_x l_x.
@@ -883,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o[i] = sees ? o[i] * inv : 0.0f;
                     if (!store)
                         continue;
-                    const int64_t at = q_row * a.out_row_stride + head * a.out_head_stride + col;
+                    const int64_t at = row_at + col;
                     if (a.out_dtype == RKV_DTYPE_F32) {
                         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
                         dst[0] = make_float4(o[0], o[1], o[2], o[3]);
@@ -900,33 +909,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 continue;
             }
-            const float inv = sees ? 1.0f / l : 0.0f;
             if (store && a.lse)
-                a.lse[q_row * a.Hq + head] = sees ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                a.lse[q_row * a.Hq + head] = log_sum;
             // Rows go out through a small staging area of the warp, 64 bytes of each at a time, so that four lanes store
             // neighbouring pieces of one row (a lane storing its own row touches 32 lines per instruction: 4800 cycles
-            // an item).  16-byte pieces are swizzled by the row against bank conflicts.
+            // an item instead of 2600).  16-byte pieces are swizzled by the row against bank conflicts.
             const uint32_t rows = __ballot_sync(0xffffffffu, store);
-            const int64_t row_at = q_row * a.out_row_stride + head * a.out_head_stride;   // elements
             unsigned char* st = sm + L::stage + (warp - 4) * kStage;
             const bool f32 = a.out_dtype == RKV_DTYPE_F32;
-            const int chunk = f32 ? 16 : 32;                // columns of 64 bytes
-#pragma unroll 1
-            for (int x = 0; rows != 0 && x < D; x += chunk) {
-                uint32_t w[16];
-                if (f32) {
-                    float o[16];
-                    tmem_ld16(tm_o + x, o);
+            unsigned char* to[4];                           // this lane's pieces: rows 8 i + lane / 4
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = __float_as_uint(sees ? o[i] * inv : 0.0f);
-                } else {
-                    float o[32];
-                    tmem_ld32(tm_o + x, o);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = sees ? pack2<kF16>(o[2 * i] * inv, o[2 * i + 1] * inv) : 0u;
-                }
+            for (int i = 0; i < 4; ++i)
+                to[i] = static_cast<unsigned char*>(a.out) + 16 * (lane & 3) +
+                        __shfl_sync(0xffffffffu, row_at, 8 * i + (lane >> 2)) * (f32 ? 4 : 2);
+            auto put = [&](const uint32_t (&w)[16], int col_bytes) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4*>(st + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
@@ -934,13 +930,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int src = 8 * i + (lane >> 2), piece = lane & 3;   // row of the warp, 16 bytes of its 64
-                    const uint4 v = *reinterpret_cast<const uint4*>(st + src * 64 + ((piece ^ ((src >> 1) & 3)) << 4));
-                    const int64_t at = __shfl_sync(0xffffffffu, row_at, src) + x;
+                    const int src = 8 * i + (lane >> 2);    // row of the warp
+                    const uint4 v = *reinterpret_cast<const uint4*>(st + src * 64 + (((lane & 3) ^ ((src >> 1) & 3)) << 4));
                     if (rows >> src & 1u)
-                        *reinterpret_cast<uint4*>(static_cast<unsigned char*>(a.out) + at * (f32 ? 4 : 2) + 16 * piece) = v;
+                        *reinterpret_cast<uint4*>(to[i] + col_bytes) = v;
                 }
                 __syncwarp();
+            };
+#pragma unroll 1
+            for (int x = 0; rows != 0 && x < D; x += 64) {
+                float o[64];
+                tmem_ld32_async(tm_o + x, o);
+                tmem_ld32_async(tm_o + x + 32, o + 32);
+                tmem_ld_wait();
+                tmem_arrived(o);
+                tmem_arrived(o + 32);
+                uint32_t w[16];
+                if (f32) {
+#pragma unroll
+                    for (int y = 0; y < 64; y += 16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = __float_as_uint(sees ? o[y + i] * inv_l : 0.0f);
+                        put(w, 4 * (x + y));
+                    }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 64; y += 32) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = sees ? pack2<kF16>(o[y + 2 * i] * inv_l, o[y + 2 * i + 1] * inv_l) : 0u;
+                        put(w, 2 * (x + y));
+                    }
+                }
             }
             // the next item's first product overwrites O: it is ordered behind these loads by p_ready
             tc_fence_before();
