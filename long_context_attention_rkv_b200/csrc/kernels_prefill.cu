@@ -23,8 +23,8 @@
 //     almost no step waits for the product before it;
 //   - a share of the exponentials runs on the FMA pipes (exp2_pair below).
 //
-// Work split: items (sequence, pair of query tiles, kv-head), sequences sorted by their number of keys and pairs
-// from the last (most keys) to the first, taken in snake order by one persistent CTA per SM.  Everything is
+// Work split: items (sequence, pair of query tiles, kv-head) from those with many keys to those with few (Schedule
+// below), taken in snake order by one persistent CTA per SM.  Everything is
 // derived from the offsets on the device, so a captured graph follows them.  Few items over many keys (the next
 // tokens of a long request) are split along the keys: the CTAs of a cluster each take a range of an item's key tiles
 // and join their parts through their shared memory (split_of says when), without a workspace.
@@ -64,6 +64,7 @@ constexpr float kBias = kF16 ? 7.0f : 0.0f;
 
 struct PrefillArgs {
     int32_t Hq, Hkv, G, batch, ntok, out_dtype, kv_padded;
+    int32_t level_keys;                 // whole prompts of at most so many tokens in all are worked on level by level
     float c;
     int64_t q_rows, kv_rows, out_row_stride, out_head_stride;
     const int32_t* q_off;
@@ -346,13 +347,24 @@ __device__ __forceinline__ Seq sequence(const PrefillArgs& a, int b)
 
 static_assert(RKV_MAX_BATCH <= kThreads - 32, "make_schedule and the barriers' set-up use other warps");
 
+// Pairs of query tiles in the order in which they are worked on, sequences sorted by their keys.  The order is balanced
+// if the work falls from item to item.
+//   - Whole prompts (L = n): the keys of a pair grow with its index from the start ("level"), so all sequences' pairs go
+//     by level, the highest first: k sequences have the levels between the k-th and the (k + 1)-th one's counts of pairs.
+//     8 ragged prompts of 300 to 2500 tokens (28 / 4 heads, 8.4 items per CTA): 99 us sequence by sequence, 92 us so.
+//     CTAs that work on different sequences share no K and V, so only where all of them stay in L2 (level_keys).
+//   - Otherwise (more keys than queries: a sequence's pairs are alike, or too many of them): sequence by sequence, each
+//     from its last pair to the first.
 struct Schedule {
     Seq seq[RKV_MAX_BATCH];
     int key[RKV_MAX_BATCH];             // keys of sequence b, for the order
     int order[RKV_MAX_BATCH];           // sequences by their keys, most first
-    int pairs[RKV_MAX_BATCH + 1];       // tile pairs before the i-th sequence of that order
-    int warp_tot[kThreads / 32];
+    int pairs[RKV_MAX_BATCH + 1];       // pairs before the i-th sequence of that order, or above the i-th one's levels
+    int warp_tot[kThreads / 32], warp_keys[kThreads / 32];
+    int by_level;
 };
+
+__device__ __forceinline__ int pairs_of(const PrefillArgs& a, const Seq& q) { return (q.n + 2 * a.ntok - 1) / (2 * a.ntok); }
 
 // Sorts the sequences and counts their tile pairs (whole CTA).
 __device__ __forceinline__ void make_schedule(const PrefillArgs& a, Schedule& s)
@@ -366,7 +378,7 @@ __device__ __forceinline__ void make_schedule(const PrefillArgs& a, Schedule& s)
         if (!q.ok && blockIdx.x == 0)
             report(a.err, RKV_ERR_INVALID_ARG);
     }
-    __syncthreads();
+    const bool whole = __syncthreads_and(q.L == q.n);
     if (tid < a.batch) {
         int rank = 0;
 #pragma unroll 8
@@ -375,21 +387,31 @@ __device__ __forceinline__ void make_schedule(const PrefillArgs& a, Schedule& s)
         s.order[rank] = tid;
     }
     __syncthreads();
-    int v = tid < a.batch ? (s.seq[s.order[tid]].n + 2 * a.ntok - 1) / (2 * a.ntok) : 0;
+    int v = tid < a.batch ? pairs_of(a, s.seq[s.order[tid]]) : 0;
+    const int next = tid + 1 < a.batch ? pairs_of(a, s.seq[s.order[tid + 1]]) : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int n = __shfl_up_sync(0xffffffffu, v, o);
         v += lane >= o ? n : 0;
     }
-    if (lane == 31)
+    const int keys = __reduce_add_sync(0xffffffffu, min(q.L, 1 << 22));
+    if (lane == 31) {
         s.warp_tot[warp] = v;
+        s.warp_keys[warp] = keys;
+    }
     __syncthreads();
-    for (int w = 0; w < warp; ++w)
-        v += s.warp_tot[w];
+    int all_keys = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        v += w < warp ? s.warp_tot[w] : 0;
+        all_keys += s.warp_keys[w];
+    }
+    const bool by_level = whole && all_keys <= a.level_keys;
     if (tid < a.batch)
-        s.pairs[tid + 1] = v;
-    if (tid == 0)
+        s.pairs[tid + 1] = by_level ? v - (tid + 1) * next : v;
+    if (tid == 0) {
         s.pairs[0] = 0;
+        s.by_level = by_level;
+    }
     __syncthreads();
 }
 
@@ -407,33 +429,47 @@ struct Item {
     __device__ __forceinline__ int last_width(int t) const { return ((last_key(t) % kN) + 16) & ~15; }
 };
 
-// The r-th item of worker p of P (CTAs or clusters); false if there is none (with the snake order only the last
-// round can lack one).
-__device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& sc, unsigned P, unsigned p, int r, Item& it)
+// The r-th item of worker p of P (CTAs or clusters): sequence, kv-head and pair; all ones if there is none (with the snake
+// order only the last round can lack one).  Out of line: inlined into five places it costs more in instruction fetches
+// (all roles run at once) than a call.
+constexpr uint64_t kNoItem = ~0ull;
+__device__ __noinline__ uint64_t find_item(const Schedule* sc, unsigned batch, unsigned n_kv_heads, unsigned ntok2, unsigned P,
+                                           unsigned p, unsigned r)
 {
-    const unsigned total = static_cast<unsigned>(sc.pairs[a.batch]) * a.Hkv;
+    const unsigned total = static_cast<unsigned>(sc->pairs[batch]) * n_kv_heads;
     const unsigned idx = r * P + ((r & 1) ? P - 1 - p : p);
     if (idx >= total)
-        return false;
-    const int pr = static_cast<int>(idx / static_cast<unsigned>(a.Hkv));
-    it.kvh = static_cast<int>(idx) - pr * a.Hkv;
-    int lo = 0, hi = a.batch - 1;
+        return kNoItem;
+    const unsigned pr = idx / n_kv_heads, kvh = idx - pr * n_kv_heads;
+    unsigned lo = 0, hi = batch - 1;
     while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (sc.pairs[mid] <= pr)
+        const unsigned mid = (lo + hi + 1) >> 1;
+        if (static_cast<unsigned>(sc->pairs[mid]) <= pr)
             lo = mid;
         else
             hi = mid - 1;
     }
-    const int b = sc.order[lo];
+    const unsigned off = pr - sc->pairs[lo], side = sc->by_level ? lo + 1 : 1, down = off / side;
+    const unsigned b = sc->order[sc->by_level ? off - down * side : lo];
+    const unsigned pair = (sc->seq[sc->order[lo]].n + ntok2 - 1) / ntok2 - 1 - down;
+    return (static_cast<uint64_t>(kvh) << 40) | (static_cast<uint64_t>(b) << 32) | pair;
+}
+
+__device__ __forceinline__ bool get_item(const PrefillArgs& a, const Schedule& sc, unsigned P, unsigned p, int r, Item& it)
+{
+    const uint64_t f = find_item(&sc, a.batch, a.Hkv, 2 * a.ntok, P, p, r);
+    if (f == kNoItem)
+        return false;
+    const int b = static_cast<int>(f >> 32) & 0xff;
     const Seq q = sc.seq[b];
     it.q0 = q.q0;
     it.n = q.n;
     it.kv0 = q.kv0;
     it.L = q.L;
+    it.kvh = static_cast<int>(f >> 40);
     it.plane = a.kv_padded ? b : 0;
     it.ntok = a.ntok;
-    it.tok0 = (sc.pairs[lo + 1] - 1 - pr) * 2 * a.ntok;
+    it.tok0 = static_cast<int>(f) * 2 * a.ntok;
     return true;
 }
 
@@ -1080,6 +1116,7 @@ cudaError_t launch_prefill(const rkv_prefill_config& c, const void* q, const voi
     a.ntok = kM / a.G;
     a.out_dtype = c.out_dtype;
     a.kv_padded = c.kv_padded;
+    a.level_keys = static_cast<int>((int64_t(64) << 20) / (4ll * c.head_dim * c.n_kv_heads));   // half of the L2
     const double scale = c.scale > 0.0f ? c.scale : 1.0 / std::sqrt(static_cast<double>(c.head_dim));
     a.c = static_cast<float>(scale * 1.4426950408889634);
     a.q_rows = c.q_rows;

@@ -138,6 +138,31 @@ def test_prefill_keys_shared_by_a_cluster(dtype, out_dtype, hq, hkv, d, keys, ne
         assert torch.equal(first[0], out) and torch.equal(first[1], lse)
 
 
+@pytest.mark.parametrize("lens", [[450, 451, 1, 0, 300] * 8, [2049, 5, 700, 700, 64, 31, 1]])
+def test_prefill_orders_of_work(lens):
+    # 16 kv-heads: above 8192 tokens in all the sequences go one by one, below level by level; and with earlier keys
+    g = torch.Generator().manual_seed(len(lens))
+    n = sum(lens)
+    q, K, V = (values(g, (n, 16, 128), torch.bfloat16).cuda() for _ in range(3))
+    off = offsets(lens)
+    out, lse = prefill(q, K, V, off)
+    check_prefill(q, K, V, off, lambda b: (K[off[b]:off[b + 1]], V[off[b]:off[b + 1]]), out, lse)
+    half = [m // 2 for m in lens]
+    starts = offsets(half)
+    q2 = torch.cat([q[o + m - h:o + m] for o, m, h in zip(off, lens, half)])
+    out2, lse2 = prefill(q2, K, V, starts, kv_off=off)
+    for b, (o, m, h) in enumerate(zip(off, lens, half)):
+        rows = slice(starts[b], starts[b + 1])
+        k, v = K[o:o + m].cpu(), V[o:o + m].cpu()
+        allowed = torch.arange(m)[None] <= (m - h + torch.arange(h))[:, None]
+        if h == 0:
+            continue
+        want, wlse, mag, spread = ref.attention(q2[rows].cpu(), k, v, allowed)
+        tol, ltol = ref.bounds(want, mag, spread, 128, m, q.dtype, out.dtype)
+        assert ((out2[rows].double().cpu() - want).abs() <= tol).all()
+        assert ((lse2[rows].double().cpu() - wlse).abs() <= ref.lse_bound(wlse, ltol)).all()
+
+
 def test_prefill_split_calls_on_two_streams():
     # two long single-token calls at once, repeated: no state is shared
     g = torch.Generator().manual_seed(31)
