@@ -18,7 +18,7 @@
 //
 // The code is that of the correctly rounded quotient x / s.  x * r with r = fl(1 / s) is within 2^-22 (relative) of
 // it, so x * r (1 - 2^-21) and x * r (1 + 2^-21) enclose it; rounding to codes is monotone, so where both give the
-// same code that is the quotient's.  The division is done only for a piece of eight values where they differ.
+// same code that is the quotient's.  The division is done only where they differ.
 #include <cfloat>
 
 #include "kv8_common.cuh"
@@ -112,21 +112,21 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint64_t v)
     return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Eight codes by division; rare, and kept out of line so that it takes no registers from the common path.
-template <bool kE4M3>
+// Eight int8 codes by division; rare (1 piece in 2000 of normal values), and kept out of line.
 __device__ __noinline__ uint2 divide8(float4 a, float4 b, float s)
 {
     const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t o[2] = {0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        o[e >> 2] |= encode<kE4M3>(__fdiv_rn(x[e], s)) << (8 * (e & 3));
+        o[e >> 2] |= encode<false>(__fdiv_rn(x[e], s)) << (8 * (e & 3));
     return make_uint2(o[0], o[1]);
 }
 
-// Eight codes of x / s; lo, hi: pairs of the factors that enclose 1 / s.  exact: by division whatever they say.
+// Eight codes of x / s; lo, hi: pairs of the factors that enclose 1 / s.  open: nonzero bytes where they leave the code
+// open (int8: all eight if one of them is).
 template <bool kE4M3>
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, uint64_t lo, uint64_t hi, bool exact)
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint64_t lo, uint64_t hi, uint2& open)
 {
     uint32_t o[2];
     if constexpr (kE4M3) {
@@ -137,7 +137,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, uint64_
             o[i] = e4m3_pair(mul2(a, lo)) | (e4m3_pair(mul2(b, lo)) << 16);
             p[i] = e4m3_pair(mul2(a, hi)) | (e4m3_pair(mul2(b, hi)) << 16);
         }
-        exact |= o[0] != p[0] || o[1] != p[1];
+        open = make_uint2(o[0] ^ p[0], o[1] ^ p[1]);
     } else {
         // x * f + 1.5 2^23, rounded once, holds rint(x * f) in its low bits
         const uint64_t magic = pair(12582912.0f, 12582912.0f);
@@ -151,15 +151,40 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float s, uint64_
             u[2 * i] = static_cast<uint32_t>(l);
             u[2 * i + 1] = static_cast<uint32_t>(l >> 32);
         }
-        exact |= differ != 0;
+        open.x = open.y = differ != 0 ? ~0u : 0u;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             o[i] = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040), __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040),
                                0x5410);
     }
-    if (exact)
-        return divide8<kE4M3>(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), s);
     return make_uint2(o[0], o[1]);
+}
+
+// e4m3: the codes of the open bytes by division, one by one; v: the values as 16-bit words, the first in the low half of
+// v.x.  Quotients of two 8-bit significands times 448 = 7 * 64 lie on a border of 4-bit codes often (one value in a
+// few hundred, so most warps see one): dividing whole pieces costs 32768 tokens x 8 heads x 128 4 us more.
+template <bool kF16>
+__device__ __forceinline__ void settle(const uint4& v, float s, uint2& o, uint2 open)
+{
+    while (open.x | open.y) {
+        const bool up = open.x == 0;
+        const int shift = (__ffs(up ? open.y : open.x) - 1) & ~7;
+        const uint32_t word = up ? (shift < 16 ? v.z : v.w) : (shift < 16 ? v.x : v.y);
+        const uint32_t half = shift & 8 ? word >> 16 : word & 0xffffu;
+        float x;
+        if constexpr (kF16)
+            x = __half2float(__ushort_as_half(static_cast<unsigned short>(half)));
+        else
+            x = bf16_bits_to_f32(half);
+        const uint32_t code = encode<true>(__fdiv_rn(x, s)) << shift, keep = ~(0xffu << shift);
+        if (up) {
+            o.y = (o.y & keep) | code;
+            open.y &= keep;
+        } else {
+            o.x = (o.x & keep) | code;
+            open.x &= keep;
+        }
+    }
 }
 
 // A word of two 16-bit values: the largest finite magnitude, NaN turned into 0.
@@ -321,7 +346,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) kv8_store_kernel(co
                 if (tid + j * kThreads < n * kCols) {
                     float f[8];
                     widen<kF16>(v[j], f);
-                    const uint2 o = s > 0.0f ? quantise8<kE4M3>(f, s, lo, hi, exact) : make_uint2(0, 0);
+                    uint2 open, o = quantise8<kE4M3>(f, lo, hi, open);
+                    if (exact)
+                        open = make_uint2(~0u, ~0u);
+                    if (!(s > 0.0f))
+                        o = open = make_uint2(0, 0);
+                    if constexpr (kE4M3) {
+                        settle<kF16>(v[j], s, o, open);
+                    } else {
+                        if (open.x)
+                            o = divide8(make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7]), s);
+                    }
                     *reinterpret_cast<uint2*>(dst + j * (kThreads / kCols) * D) = o;
                 }
             }
