@@ -10,9 +10,8 @@
 //
 // Bound by HBM: 2 bytes read and 1 written per element.  One CTA does the K or the V side of the runs
 // that start in one window of packed rows, for one head; it holds a run (at most one block of rows) in
-// registers between the maximum and the codes, so the rows are read once.  A window is one block's worth of
-// rows for prompts (then it holds about one run) and a single row for decode steps (every row is a run of
-// its own and all of them go side by side).  The CTA has block * head_dim / 64 threads, so that each holds
+// registers between the maximum and the codes, so the rows are read once.  A window is about one run long (window_of
+// below): one block's worth of rows for prompts, a single row for decode steps, so that all runs go side by side.  The CTA has block * head_dim / 64 threads, so that each holds
 // eight 16-byte pieces of a full block: small CTAs, many of them per SM, keep loads in flight while others
 // reduce and convert.
 //
@@ -385,6 +384,23 @@ cudaError_t launch_t(const StoreArgs& a, bool f16, dim3 grid, cudaStream_t st)
     }
 }
 
+// Rows of a window: the rows of a request where all have equally many (at most a block), as a power of two, so that a
+// window has about one run: a CTA does several runs one after the other, and a CTA without a run costs its look at the
+// slots.  Fewer rows where that leaves less than four of these small CTAs per SM.  8 heads x 128, blocks of 64, windows
+// of 1 / 4 / 16 / 64 rows: 64 requests with 1 token each 4.6 us, in windows of 64 66 us; with 4 to 8 9.8 / 6.3 / 7.0 /
+// 16.8 us; with 12 to 24 20.6 / 9.9 / 7.0 / 9.5 us; 4 with 100 to 200 10.8 / 6.0 / 4.4 / 6.7 us; 1 with 32768 411 us in
+// windows of 1, 39.4 us in windows of 64.
+int window_of(int64_t n_rows, const rkv_kv8_cache& c)
+{
+    constexpr int64_t kManyCtas = 4 * 148;
+    int w = 1;
+    while (2 * w <= c.block_size && 2ll * w * c.batch <= n_rows)
+        w *= 2;
+    while (w > 1 && 2ll * c.n_kv_heads * ((n_rows + w - 1) / w) < kManyCtas)
+        w /= 2;
+    return w;
+}
+
 }  // namespace
 
 cudaError_t launch_kv8_store(const rkv_kv8_cache& c, const void* K_new, const void* V_new, int64_t row_stride,
@@ -396,9 +412,7 @@ cudaError_t launch_kv8_store(const rkv_kv8_cache& c, const void* K_new, const vo
     while ((1 << a.shift) < c.block_size)
         ++a.shift;
     a.n_blocks = c.n_blocks;
-    // up to a few rows per request (a decode step): every row a window, so that no CTA does several
-    // runs one after the other; otherwise about one run per window
-    a.window = n_rows <= 4ll * c.batch ? 1 : c.block_size;
+    a.window = window_of(n_rows, c);
     a.row_stride = row_stride;
     a.head_stride = head_stride;
     a.n_rows = n_rows;

@@ -138,9 +138,9 @@ def test_prefill_keys_shared_by_a_cluster(dtype, out_dtype, hq, hkv, d, keys, ne
         assert torch.equal(first[0], out) and torch.equal(first[1], lse)
 
 
-@pytest.mark.parametrize("lens", [[450, 451, 1, 0, 300] * 8, [2049, 5, 700, 700, 64, 31, 1]])
+@pytest.mark.parametrize("lens", [[450, 451, 1, 0, 300] * 11, [2049, 5, 700, 700, 64, 31, 1]])
 def test_prefill_orders_of_work(lens):
-    # 16 kv-heads: above 8192 tokens in all the sequences go one by one, below level by level; and with earlier keys
+    # 16 kv-heads: above 12288 tokens in all the sequences go one by one, below level by level; and with earlier keys
     g = torch.Generator().manual_seed(len(lens))
     n = sum(lens)
     q, K, V = (values(g, (n, 16, 128), torch.bfloat16).cuda() for _ in range(3))
