@@ -26,6 +26,9 @@
 // its largest element lies in [2^14, 2^15): every element is then exact or, if tiny, off by at most 2^-40 of
 // the largest.
 //
+// Measured: 4 requests of 131072 tokens, 32 / 8 heads of 128: 183 us = 5.85 TB/s (0.90 of the measured copy rate); 8 ragged
+// requests of 16384 to 32768, 28 / 4 heads: 47.7 us; one of 2049: 8.8 us, latency of the two launches.
+//
 // Work split: units (request, kv-head) are cut into tiles of 64 tokens; the CTAs take equal contiguous
 // ranges of all tiles, found from the lengths on the device.  A CTA's four warps take 16 tokens of each
 // tile; at the end of a unit its warps' states are merged and either written out (the CTA had the whole
