@@ -408,6 +408,34 @@ def test_tables_refuse_without_taking():
     assert int(t.n_free) == 5 and torch.equal(t.lengths, before[1])
 
 
+@pytest.mark.parametrize("batch,new,room", [(5, 2000, 12000), (3, 10, 40), (200, 9, 2000)])
+def test_tables_replayed_in_place(batch, new, room):
+    # a captured call that grows its own lengths, for the one-CTA forms and the one with a second launch; two such graphs
+    # replayed in turn on two table sets
+    r = random.Random(batch)
+    block, width = 32, 400
+    sets = [(rkv.BlockTables(batch, width, block, 9000), ref.Tables(batch, width, block, 9000)) for _ in range(2)]
+    counts = ints([0] * batch)
+    slots = torch.zeros(room, dtype=torch.int32, device="cuda")
+    graphs = []
+    for t, _ in sets:
+        t.extend(counts, slots)                      # nothing new: also loads the kernels
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            t.extend(counts, slots)
+        graphs.append(g)
+    for step in range(6):
+        t, want = sets[step % 2]
+        add = [r.randint(0, new) for _ in range(batch)]
+        counts.copy_(ints(add))
+        graphs[step % 2].replay()
+        ws, _ = want.extend(add)
+        assert slots.tolist() == ws + [-1] * (room - len(ws))
+        check_tables(t, want)
+        assert t.device_error() == 0
+
+
 def test_tables_report_block_ids_outside_the_pool():
     t = rkv.BlockTables(1, 4, 16, 6)
     t.free_list[5] = 6
@@ -732,6 +760,36 @@ def test_decode_reports_corruption():
     cache.decode(q, table.cuda(), ints([100, -3]), out)
     assert cache.device_error() == corrupt
     assert torch.equal(out[0], want[0]) and (out[1] == 0).all()
+
+
+def test_decode_graphs_that_share_a_workspace_and_blocks():
+    # two captured steps of one cache (one workspace), replayed in turn; requests that share a prefix's blocks; the
+    # same request twice
+    g = torch.Generator().manual_seed(14)
+    lens = [3000, 3000, 2999, 70]
+    cache, table = random_cache(g, "e4m3", lens, 128, 2, 8, 64, torch.bfloat16)
+    table[1] = table[0]
+    table[2, :40] = table[0, :40]
+    q = [values(g, (4, 8, 128), torch.bfloat16).cuda() for _ in range(2)]
+    q[0][1] = q[0][0]
+    t, n = table.cuda(), ints(lens)
+    outs, graphs = [torch.empty_like(x) for x in q], []
+    for x, o in zip(q, outs):
+        cache.decode(x, t, n, o)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cache.decode(x, t, n, o)
+        graphs.append(graph)
+    want = [o.clone() for o in outs]
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
+    assert torch.equal(want[0][0], want[0][1])
+    assert cache.device_error() == 0
+    for x, o in zip(q, want):
+        check_decode(cache, table, lens, x, o)
 
 
 def test_decode_on_two_streams_with_their_own_workspaces():
