@@ -486,7 +486,7 @@ class Prefill:
         if not (q.dtype is dt and K.dtype is dt and V.dtype is dt and out.dtype is self._out and q.is_contiguous() and
                 K.is_contiguous() and V.is_contiguous() and out.is_contiguous() and q.numel() >= self._q_reach and
                 K.numel() >= kv and V.numel() >= kv and out.numel() >= self._out_reach):
-            # strided views, or something to refuse
+            # strided views, or one of them is refused
             where = "Prefill.attend"
             _need(where, "q", q, self._q_reach, dt, True)
             _need(where, "K", K, kv, dt, True)
@@ -594,12 +594,14 @@ class KV8Cache:
         """q, out: [batch, q_heads, head_dim]; block_table: int32 [batch, max_blocks]; lengths: int32 [batch]; all
         contiguous.  One workspace: calls on several streams must not overlap."""
         n, n_table, n_len = self._sizes
-        if not (q.dtype is self._in and out.dtype is self._out and q.numel() >= n and out.numel() >= n and
-                q.is_contiguous() and out.is_contiguous()):
+        i32 = self._i32
+        if not (q.dtype is self._in and out.dtype is self._out and block_table.dtype is i32 and lengths.dtype is i32 and
+                q.numel() >= n and out.numel() >= n and block_table.numel() >= n_table and lengths.numel() >= n_len and
+                q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous() and lengths.is_contiguous()):
             _need("KV8Cache.decode", "q", q, n, self._in)
             _need("KV8Cache.decode", "out", out, n, self._out)
-        _need("KV8Cache.decode", "block_table", block_table, n_table, self._i32)
-        _need("KV8Cache.decode", "lengths", lengths, n_len, self._i32)
+            _need("KV8Cache.decode", "block_table", block_table, n_table, i32)
+            _need("KV8Cache.decode", "lengths", lengths, n_len, i32)
         self._here("KV8Cache.decode")
         rkv_kv8_decode_attn(self.c, q, block_table, lengths, out, self.workspace, self.workspace.numel(), stream)
 

@@ -8,6 +8,7 @@ import numpy as np
 import torch
 
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+FIXED_HALF_STEP = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -150}   # below the normal range
 QMAX = {"int8": 127.0, "e4m3": 448.0}
 KIND = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
 
@@ -46,7 +47,8 @@ def bounds(out, mag, spread, d, keys, weight_type, out_type, floor=0.0):
     after the division).  Weights are rounded to weight_type (half a step), the exponential is good to 2^-21 with
     its argument's rounding (|x| <= 2^3 above the running maximum; below it the weight shrinks faster than the
     argument's step grows: x 2^-23 2^x <= 2^-23), and the two sums over the keys add 2^-23 a key each.  All of it
-    is relative to sum p|v| / sum p; then the output's own half step.
+    is relative to sum p|v| / sum p; then the output's own half step (a fixed one where the output is below its type's
+    normal range).
 
     floor: a binary16 weight below 2^-14 has the fixed step 2^-24 instead of a relative one, so it is off by up to
     2^-25, whatever its size.  The largest weight w of a row is kept as at least 2^k (2^15 in the decode, 2^7 in
@@ -55,7 +57,7 @@ def bounds(out, mag, spread, d, keys, weight_type, out_type, floor=0.0):
     the largest scale times qmax.  floor is 2^-(25 + k) max|v|."""
     logit = (d + 2) * 2.0 ** -23 * spread
     rel = 2 * logit + 2 * HALF_STEP[weight_type] * 0.5 + 2.0 ** -20 + 2 * keys * 2.0 ** -23
-    tol = mag * rel[..., None] + HALF_STEP[out_type] * out.abs() + keys * floor + 1e-30
+    tol = mag * rel[..., None] + HALF_STEP[out_type] * out.abs() + FIXED_HALF_STEP[out_type] + keys * floor + 1e-30
     return tol, logit + 2.0 ** -20 + keys * 2.0 ** -23
 
 
