@@ -27,12 +27,13 @@
 // the largest.
 //
 // Measured: 4 requests of 131072 tokens, 32 / 8 heads of 128: 183 us = 5.85 TB/s (0.90 of the measured copy rate); 8 ragged
-// requests of 16384 to 32768, 28 / 4 heads: 47.7 us; one of 2049: 8.8 us, latency of the two launches.
+// requests of 16384 to 32768, 28 / 4 heads: 47.7 us; one of 2049: 7.5 us, latency.
 //
-// Work split: units (request, kv-head) are cut into tiles of 64 tokens; the CTAs take equal contiguous
-// ranges of all tiles, found from the lengths on the device.  A CTA's four warps take 16 tokens of each
-// tile; at the end of a unit its warps' states are merged and either written out (the CTA had the whole
-// unit) or left in the workspace for the join kernel, which adds the parts in order.
+// Work split: units (request, kv-head) are cut into tiles of 64 tokens; a CTA's four warps take 16 tokens of each tile, and
+// at the end of a unit their states are merged.  Short rows: a cluster per unit, whose CTAs take equal ranges of its tiles
+// and join through their shared memory (cluster_parts says when).  Otherwise the CTAs take equal contiguous ranges of
+// all tiles, found from the lengths on the device, and what is not a whole unit is left in the workspace for the join
+// kernel, which adds the parts in order.
 #include <cuda_fp8.h>
 
 #include <cfloat>
@@ -231,44 +232,99 @@ __device__ __forceinline__ void store_out(void* out, int dtype, int64_t e, float
         static_cast<uint16_t*>(out)[e] = f32_to_bf16_bits(v);
 }
 
-// NT: tiles of 8 query heads (G <= 8 * NT).
-template <int D, bool kE4M3, bool kF16, int NT>
+// ---- clusters ----
+
+__device__ __forceinline__ int cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return static_cast<int>(r);
+}
+
+__device__ __forceinline__ int cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return static_cast<int>(r);
+}
+
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A float of the shared memory of CTA `rank` of the cluster, at this CTA's address p.
+__device__ __forceinline__ float peer_float(const float* p, int rank)
+{
+    uint32_t at;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+constexpr int kMaxParts = 8;           // CTAs of a cluster: the largest portable one
+
+// NT: tiles of 8 query heads (G <= 8 * NT).  kCluster: a cluster per unit, whose CTAs take equal ranges of its tiles and
+// join their parts through their shared memory; otherwise equal ranges of all tiles and the workspace.
+template <int D, bool kE4M3, bool kF16, int NT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode_kernel(const DecodeArgs a)
 {
     constexpr int kSteps = D / 16;               // K-side products per 16 tokens; also V row tiles
     constexpr int kHeads = 8 * NT;
-    __shared__ int64_t pre[RKV_MAX_BATCH + 1];
+    __shared__ int64_t pre[kCluster ? 1 : RKV_MAX_BATCH + 1];
+    __shared__ float s_part[kCluster ? kHeads * D : 1], s_part_m[kHeads], s_part_l[kHeads];   // this CTA's part
     __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
     __shared__ float s_o[kWarps][kHeads][D + 4];
     __shared__ float s_qs[kHeads];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    tile_prefix(a, pre);
-    const int64_t total = pre[a.batch];
-    const int p = blockIdx.x, P = workers(total, gridDim.x);
-    int64_t lo = p < P ? first_tile(total, p, P) : 0;
-    const int64_t range_lo = lo, hi = p < P ? first_tile(total, p + 1, P) : 0;
+    const int p = blockIdx.x;
+    int64_t lo = 0, range_lo = 0, hi = 1;
     bool corrupt = false;
-    if (p == 0)
-        for (int b = tid; b < a.batch; b += kThreads)
-            corrupt |= a.lengths[b] != request_len(a, b);
+    if constexpr (!kCluster) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        tile_prefix(a, pre);
+        const int64_t total = pre[a.batch];
+        const int P = workers(total, gridDim.x);
+        lo = range_lo = p < P ? first_tile(total, p, P) : 0;
+        hi = p < P ? first_tile(total, p + 1, P) : 0;
+        if (p == 0)
+            for (int b = tid; b < a.batch; b += kThreads)
+                corrupt |= a.lengths[b] != request_len(a, b);
+    }
 
     while (lo < hi) {
-        // ---- the unit of tile lo and this CTA's part of it
-        int b0 = 0, b1 = a.batch - 1;
-        while (b0 < b1) {
-            const int mid = (b0 + b1 + 1) >> 1;
-            if (pre[mid] <= lo)
-                b0 = mid;
-            else
-                b1 = mid - 1;
+        // ---- the unit and this CTA's part of it
+        int b, kvh, t_lo, t_hi;
+        int64_t u_lo = 0;
+        if constexpr (kCluster) {
+            const int unit = p / cluster_size();
+            b = unit / a.Hkv;
+            kvh = unit - b * a.Hkv;
+        } else {
+            int b0 = 0, b1 = a.batch - 1;
+            while (b0 < b1) {
+                const int mid = (b0 + b1 + 1) >> 1;
+                if (pre[mid] <= lo)
+                    b0 = mid;
+                else
+                    b1 = mid - 1;
+            }
+            b = b0;
         }
-        const int b = b0, len = request_len(a, b);
+        const int len = request_len(a, b);
         const int nt = (len + kTile - 1) / kTile;
-        const int kvh = static_cast<int>((lo - pre[b]) / nt);
-        const int64_t u_lo = pre[b] + static_cast<int64_t>(kvh) * nt, u_hi = u_lo + nt;
-        const int t_lo = static_cast<int>(lo - u_lo), t_hi = static_cast<int>(min(hi, u_hi) - u_lo);
+        if constexpr (kCluster) {
+            t_lo = nt * cluster_rank() / cluster_size();
+            t_hi = nt * (cluster_rank() + 1) / cluster_size();
+            corrupt |= a.lengths[b] != len;
+        } else {
+            kvh = static_cast<int>((lo - pre[b]) / nt);
+            u_lo = pre[b] + static_cast<int64_t>(kvh) * nt;
+            t_lo = static_cast<int>(lo - u_lo);
+            t_hi = static_cast<int>(min(hi, u_lo + nt) - u_lo);
+        }
         const int32_t* row = a.table + static_cast<int64_t>(b) * a.max_blocks;
         const uint16_t* qu = a.q + (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(kvh) * a.G) * D;
 
@@ -492,7 +548,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                 L = fmaf(s_l[w][head], f, L);
                 O = fmaf(s_o[w][head][ch], f, O);
             }
-            if (whole) {
+            if constexpr (kCluster) {
+                s_part[x] = O;
+                if (ch == 0) {
+                    s_part_m[head] = M;
+                    s_part_l[head] = L;
+                }
+            } else if (whole) {
                 store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
                           L != 0.0f ? O / L : 0.0f);
             } else {
@@ -501,8 +563,38 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                     a.part_ml[part + head] = make_float2(M, L);
             }
         }
-        __syncthreads();
-        lo = u_lo + t_hi;
+        if constexpr (kCluster) {
+            cluster_sync_all();                              // the parts of all CTAs are there
+            const int parts = cluster_size();
+            for (int x = cluster_rank() * kThreads + tid; x < a.G * D; x += parts * kThreads) {
+                const int head = x / D, ch = x % D;
+                float m_[kMaxParts], l_[kMaxParts], o_[kMaxParts];
+                float M = kNone, L = 0.0f, O = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kMaxParts; ++r) {
+                    m_[r] = r < parts ? peer_float(&s_part_m[head], r) : kNone;
+                    l_[r] = r < parts ? peer_float(&s_part_l[head], r) : 0.0f;
+                    o_[r] = r < parts ? peer_float(&s_part[x], r) : 0.0f;
+                }
+#pragma unroll
+                for (int r = 0; r < kMaxParts; ++r)
+                    M = fmaxf(M, m_[r]);
+#pragma unroll
+                for (int r = 0; r < kMaxParts; ++r) {
+                    const float f = ex2(m_[r] - M);
+                    L = fmaf(l_[r], f, L);
+                    O = fmaf(o_[r], f, O);
+                }
+                store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
+                          L != 0.0f ? O / L : 0.0f);
+            }
+            __syncthreads();
+            cluster_sync_all();                              // no CTA leaves while others read its part
+            break;
+        } else {
+            __syncthreads();
+            lo = u_lo + t_hi;
+        }
     }
     if (__any_sync(0xffffffffu, corrupt) && lane == 0)
         report(a.err, RKV_ERR_CORRUPT);
@@ -596,13 +688,32 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, 
     }
 }
 
-template <int D, bool kE4M3, bool kF16>
-cudaError_t launch_t(const DecodeArgs& a, int ctas, cudaStream_t st)
+template <int D, bool kE4M3, bool kF16, int NT>
+cudaError_t launch_cluster(const DecodeArgs& a, int parts, cudaStream_t st)
 {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.batch * a.Hkv * parts);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv8_decode_kernel<D, kE4M3, kF16, NT, true>, a);
+}
+
+template <int D, bool kE4M3, bool kF16>
+cudaError_t launch_t(const DecodeArgs& a, int ctas, int parts, cudaStream_t st)
+{
+    if (parts > 0)
+        return a.G <= 8 ? launch_cluster<D, kE4M3, kF16, 1>(a, parts, st) : launch_cluster<D, kE4M3, kF16, 2>(a, parts, st);
     if (a.G <= 8)
-        kv8_decode_kernel<D, kE4M3, kF16, 1><<<ctas, kThreads, 0, st>>>(a);
+        kv8_decode_kernel<D, kE4M3, kF16, 1, false><<<ctas, kThreads, 0, st>>>(a);
     else
-        kv8_decode_kernel<D, kE4M3, kF16, 2><<<ctas, kThreads, 0, st>>>(a);
+        kv8_decode_kernel<D, kE4M3, kF16, 2, false><<<ctas, kThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
@@ -619,11 +730,29 @@ cudaError_t launch_t(const DecodeArgs& a, int ctas, cudaStream_t st)
 }
 
 template <int D>
-cudaError_t launch_d(const DecodeArgs& a, bool e4m3, bool f16, int ctas, cudaStream_t st)
+cudaError_t launch_d(const DecodeArgs& a, bool e4m3, bool f16, int ctas, int parts, cudaStream_t st)
 {
     if (e4m3)
-        return f16 ? launch_t<D, true, true>(a, ctas, st) : launch_t<D, true, false>(a, ctas, st);
-    return f16 ? launch_t<D, false, true>(a, ctas, st) : launch_t<D, false, false>(a, ctas, st);
+        return f16 ? launch_t<D, true, true>(a, ctas, parts, st) : launch_t<D, true, false>(a, ctas, parts, st);
+    return f16 ? launch_t<D, false, true>(a, ctas, parts, st) : launch_t<D, false, false>(a, ctas, parts, st);
+}
+
+// CTAs of a cluster per unit, 0 for the form with the workspace and the join kernel.  What the host knows are the units and
+// the tiles that a table row can hold, so a cluster is taken where its CTAs have at most 8 tiles even of a full row (one
+// long request among short ones then costs little), as many CTAs as run at once.  32 / 8 heads of 128, with join kernel
+// and in clusters of 1 / 2 / 4 / 8: 1 request of 512 tokens 6.7 and 10.5 / 7.2 / 5.5 / 5.0 us, of 2049 8.6 and 27 / 15.6 /
+// 10.1 / 7.5, of 8192 13.2 and 90 / 47 / 26 / 15.2; 8 of 2049 15.6 and 27 / 16.1 / 11.8 / 11.6; 64 of 1024 38.1 and 32.3 /
+// 35.5 / 43 / 61, of 2049 61 and 56 / 59 / 67 / 85.  It also saves the host a launch (2 us).
+int cluster_parts(const rkv_kv8_cache& c)
+{
+    constexpr int64_t kTiles = 8;
+    const int64_t units = static_cast<int64_t>(c.batch) * c.n_kv_heads;
+    const int64_t tiles = (static_cast<int64_t>(c.max_blocks) * c.block_size + kTile - 1) / kTile;
+    const int64_t at_once = 148 * (c.n_q_heads / c.n_kv_heads <= 8 ? kCtasPerSm : 2);
+    int parts = 1;
+    while (parts < kMaxParts && (tiles > kTiles * parts || units * 2 * parts <= at_once))
+        parts *= 2;
+    return tiles <= kTiles * parts && (parts == 1 || units * parts <= 2 * at_once) ? parts : 0;
 }
 
 // CTAs of a launch: what the SMs hold at once (the NT = 2 form holds two per SM), at most one per tile
@@ -673,7 +802,8 @@ cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32
     const int ctas = decode_ctas(c, sms);
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + 2ll * ctas * a.G * c.head_dim);
-    return c.head_dim == 128 ? launch_d<128>(a, e4m3, f16, ctas, st) : launch_d<64>(a, e4m3, f16, ctas, st);
+    const int parts = cluster_parts(c);
+    return c.head_dim == 128 ? launch_d<128>(a, e4m3, f16, ctas, parts, st) : launch_d<64>(a, e4m3, f16, ctas, parts, st);
 }
 
 }  // namespace rkv

@@ -762,6 +762,49 @@ def test_decode_reports_corruption():
     assert torch.equal(out[0], want[0]) and (out[1] == 0).all()
 
 
+@pytest.mark.parametrize("code,dtype", [("int8", torch.bfloat16), ("e4m3", torch.float16)])
+@pytest.mark.parametrize("hq,hkv,d,block", [(8, 1, 128, 16), (3, 3, 64, 32), (24, 2, 64, 64), (14, 2, 128, 128)])
+@pytest.mark.parametrize("batch", [1, 5, 40, 256])
+def test_decode_short_and_long_rows(code, dtype, hq, hkv, d, block, batch):
+    # the same requests by rows of few blocks (units by clusters) and by rows that could hold 5000 tokens (workspace)
+    g = torch.Generator().manual_seed(batch + hq)
+    r = random.Random(batch)
+    top = 500 if batch < 40 else 130
+    lens = [r.choice([0, 1, 63, 64, r.randint(0, top), top]) for _ in range(batch)]
+    cache, table = random_cache(g, code, lens, d, hkv, hq, block, dtype)
+    q = values(g, (batch, hq, d), dtype).cuda()
+    wide = torch.full((batch, -(-5000 // block)), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    shape = dict(head_dim=d, n_kv_heads=hkv, n_q_heads=hq, block_size=block, n_blocks=cache.c.n_blocks, batch=batch,
+                 code_type=KV8[code], in_dtype=CODE[dtype])
+    long = rkv.KV8Cache(rkv.make_kv8_config(max_blocks=wide.shape[1], **shape), cache.codes_K, cache.codes_V,
+                        cache.scale_K, cache.scale_V)
+    corrupt = rkv.STATUS_CODE["RKV_ERR_CORRUPT"]
+    for c, t in ((cache, table), (long, wide)):
+        out = torch.full_like(q, 7.0)
+        c.decode(q, t.cuda(), ints(lens), out)
+        assert c.device_error() == 0
+        check_decode(c, t, lens, q, out)
+        b = max(range(batch), key=lambda i: lens[i])
+        if lens[b] == 0:
+            continue
+        bad, other = t.clone(), torch.full_like(q, 7.0)
+        bad[b, 0] = -7
+        c.decode(q, bad.cuda(), ints(lens), other)
+        assert c.device_error() == corrupt
+        keep = torch.arange(batch) != b
+        assert torch.equal(other[keep], out[keep]) and other[b].isfinite().all()
+        over = list(lens)
+        over[b] = t.shape[1] * block + 1
+        full = t.clone()
+        full[b] = t[b, 0]                            # every block of the row is one of the pool
+        whole = torch.full_like(q, 7.0)
+        c.decode(q, full.cuda(), ints(over), whole)
+        assert c.device_error() == corrupt
+        # a longer request moves the others' cuts between CTAs in the form with the workspace: not bit for bit there
+        check_decode(c, t[keep], [n for i, n in enumerate(lens) if i != b], q[keep], whole[keep])
+
+
 def test_decode_graphs_that_share_a_workspace_and_blocks():
     # two captured steps of one cache (one workspace), replayed in turn; requests that share a prefix's blocks; the
     # same request twice
