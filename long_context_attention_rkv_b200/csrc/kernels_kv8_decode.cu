@@ -9,6 +9,9 @@
 // it can enter the second product as a binary16 number (11 significant bits, rounded to nearest: the same
 // or finer than a 16-bit output); the factor 2^15 keeps the weights of a flat context of millions of tokens
 // out of binary16's subnormals.
+// M is kept as the two terms of the token that attains it (Top below), and the logits are subtracted from one
+// another before anything small is added: x_i + log2 sV_blk, or 15 - M, rounded to 32 bits would be off by 8 and more
+// for logits of 2^25 and beyond, past binary16's range and with equal logits weighted by their scales.
 //
 // Both products run on warp-level tensor-core instructions (m16n8k16, binary16 in, fp32 out): with at most
 // 8 query heads per kv-head they have a single narrow column tile, 2 x 128 x 8 multiply-adds per 256 bytes, so
@@ -53,7 +56,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;     // tokens per CTA step
 constexpr int kCtasPerSm = 4;          // at 128 registers; 4 requests of 131072 tokens: 183 us, three 191 us, two 246 us
 constexpr int kMaxCtas = 160 * kCtasPerSm;
-constexpr float kNone = -FLT_MAX;      // running maximum before any token
+constexpr float kNone = -FLT_MAX;      // logit before any token
 constexpr float kWeightExp = 15.0f;    // weights are kept times 2^15: binary16 then holds 2^-39 .. 1 of the largest
 
 struct DecodeArgs {
@@ -68,7 +71,7 @@ struct DecodeArgs {
     const int32_t* lengths;
     void* out;
     float* part_o;                     // [2 * CTAs][heads][D]
-    float2* part_ml;                   // [2 * CTAs][heads]: M, L
+    float4* part_ml;                   // [2 * CTAs][heads]: M (x, s), L, unused
     int32_t* err;
 };
 
@@ -151,6 +154,32 @@ __device__ __forceinline__ float ex2(float x)
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// A maximum M = x + s: the logit and the log2 of the value scale of the token that attains it.
+struct Top {
+    float x, s;
+    // log2 of M / other: the difference of logits first, so it is right whatever their size
+    __device__ __forceinline__ float over(const Top& other) const { return (x - other.x) + (s - other.s); }
+    __device__ __forceinline__ void raise(const Top& other)
+    {
+        if (other.over(*this) > 0.0f)
+            *this = other;
+    }
+};
+
+constexpr Top kNoTop = {kNone, 0.0f};  // before any token
+
+// The highest of N (a power of two), in m[0] and returned.
+template <int N>
+__device__ __forceinline__ Top highest(Top (&m)[N])
+{
+#pragma unroll
+    for (int d = N / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < d; ++i)
+            m[i].raise(m[i + d]);
+    return m[0];
 }
 
 // Four codes of a word as two binary16 pairs (bytes 0, 1 and bytes 2, 3), exact.
@@ -253,13 +282,25 @@ __device__ __forceinline__ void cluster_sync_all()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A float of the shared memory of CTA `rank` of the cluster, at this CTA's address p.
+// A float, or four, of the shared memory of CTA `rank` of the cluster, at this CTA's address p.
 __device__ __forceinline__ float peer_float(const float* p, int rank)
 {
     uint32_t at;
     float v;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 peer_float4(const float4* p, int rank)
+{
+    uint32_t at;
+    float4 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 
@@ -273,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
     constexpr int kSteps = D / 16;               // K-side products per 16 tokens; also V row tiles
     constexpr int kHeads = 8 * NT;
     __shared__ int64_t pre[kCluster ? 1 : RKV_MAX_BATCH + 1];
-    __shared__ float s_part[kCluster ? kHeads * D : 1], s_part_m[kHeads], s_part_l[kHeads];   // this CTA's part
-    __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
+    __shared__ float s_part[kCluster ? kHeads * D : 1];                  // this CTA's part
+    __shared__ float4 s_part_ml[kHeads], s_ml[kWarps][kHeads];           // the CTA's and the warps' M (x, s), L
     __shared__ float s_o[kWarps][kHeads][D + 4];
     __shared__ float s_qs[kHeads];
 
@@ -397,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
         }
 
         float o[NT][kSteps][4];
-        float m[NT][2], l[NT][2];
+        Top m[NT][2];
+        float l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -405,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     o[n][i][x] = 0.0f;
-            m[n][0] = m[n][1] = kNone;
+            m[n][0] = m[n][1] = kNoTop;
             l[n][0] = l[n][1] = 0.0f;
         }
 
@@ -454,16 +496,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const float f = qs[n][x] * sk;
-                    sc[n][x] = in0 ? fmaf(sc[n][x], f, lsv) : -INFINITY;
-                    sc[n][2 + x] = in1 ? fmaf(sc[n][2 + x], f, lsv) : -INFINITY;
+                    sc[n][x] = in0 ? sc[n][x] * f : -INFINITY;
+                    sc[n][2 + x] = in1 ? sc[n][2 + x] * f : -INFINITY;
                     top[x] = fmaxf(sc[n][x], sc[n][2 + x]);
                     top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 4));
                     top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 8));
                     top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 16));
                 }
-                const float m0 = fmaxf(m[n][0], top[0]), m1 = fmaxf(m[n][1], top[1]);
-                if (__any_sync(0xffffffffu, m0 != m[n][0] || m1 != m[n][1])) {
-                    const float r0 = ex2(m[n][0] - m0), r1 = ex2(m[n][1] - m1);
+                float d0 = lsv - m[n][0].s, d1 = lsv - m[n][1].s;
+                const bool up0 = (top[0] - m[n][0].x) + d0 > 0.0f, up1 = (top[1] - m[n][1].x) + d1 > 0.0f;
+                if (__any_sync(0xffffffffu, up0 || up1)) {
+                    const Top m0 = up0 ? Top{top[0], lsv} : m[n][0], m1 = up1 ? Top{top[1], lsv} : m[n][1];
+                    const float r0 = ex2(m[n][0].over(m0)), r1 = ex2(m[n][1].over(m1));
                     l[n][0] *= r0;
                     l[n][1] *= r1;
 #pragma unroll
@@ -475,10 +519,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                     }
                     m[n][0] = m0;
                     m[n][1] = m1;
+                    d0 = lsv - m0.s;
+                    d1 = lsv - m1.s;
                 }
-                const float b0 = kWeightExp - m0, b1 = kWeightExp - m1;
-                const float w00 = ex2(sc[n][0] + b0), w01 = ex2(sc[n][1] + b1);
-                const float w10 = ex2(sc[n][2] + b0), w11 = ex2(sc[n][3] + b1);
+                d0 += kWeightExp;
+                d1 += kWeightExp;
+                const float w00 = ex2((sc[n][0] - m[n][0].x) + d0), w01 = ex2((sc[n][1] - m[n][1].x) + d1);
+                const float w10 = ex2((sc[n][2] - m[n][0].x) + d0), w11 = ex2((sc[n][3] - m[n][1].x) + d1);
                 l[n][0] = fmaf(w00 + w10, rsv, l[n][0]);
                 l[n][1] = fmaf(w01 + w11, rsv, l[n][1]);
                 const __half2 p0 = __floats2half2_rn(w00, w01), p1 = __floats2half2_rn(w10, w11);
@@ -519,10 +566,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
-                if (g == 0) {
-                    s_m[warp][8 * n + 2 * t + x] = m[n][x];
-                    s_l[warp][8 * n + 2 * t + x] = v;
-                }
+                if (g == 0)
+                    s_ml[warp][8 * n + 2 * t + x] = make_float4(m[n][x].x, m[n][x].s, v, 0.0f);
 #pragma unroll
                 for (int i = 0; i < kSteps; ++i) {
                     // rows g and g + 8 of row tile i: channels (D / 8) g + 2 i, + 1
@@ -537,30 +582,32 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
         const int64_t part = static_cast<int64_t>(2 * p + (head_part ? 0 : 1)) * a.G;
         for (int x = tid; x < a.G * D; x += kThreads) {
             const int head = x / D, ch = x % D;
-            float M = kNone;
+            float4 ml[kWarps];
+            Top m_[kWarps];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                M = fmaxf(M, s_m[w][head]);
+            for (int w = 0; w < kWarps; ++w) {
+                ml[w] = s_ml[w][head];
+                m_[w] = {ml[w].x, ml[w].y};
+            }
+            const Top M = highest(m_);
             float L = 0.0f, O = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(s_m[w][head] - M);
-                L = fmaf(s_l[w][head], f, L);
+                const float f = ex2(Top{ml[w].x, ml[w].y}.over(M));
+                L = fmaf(ml[w].z, f, L);
                 O = fmaf(s_o[w][head][ch], f, O);
             }
             if constexpr (kCluster) {
                 s_part[x] = O;
-                if (ch == 0) {
-                    s_part_m[head] = M;
-                    s_part_l[head] = L;
-                }
+                if (ch == 0)
+                    s_part_ml[head] = make_float4(M.x, M.s, L, 0.0f);
             } else if (whole) {
                 store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
                           L != 0.0f ? O / L : 0.0f);
             } else {
                 a.part_o[(part + head) * D + ch] = O;
                 if (ch == 0)
-                    a.part_ml[part + head] = make_float2(M, L);
+                    a.part_ml[part + head] = make_float4(M.x, M.s, L, 0.0f);
             }
         }
         if constexpr (kCluster) {
@@ -568,21 +615,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             const int parts = cluster_size();
             for (int x = cluster_rank() * kThreads + tid; x < a.G * D; x += parts * kThreads) {
                 const int head = x / D, ch = x % D;
-                float m_[kMaxParts], l_[kMaxParts], o_[kMaxParts];
-                float M = kNone, L = 0.0f, O = 0.0f;
+                float4 ml[kMaxParts];
+                Top m_[kMaxParts];
+                float o_[kMaxParts], L = 0.0f, O = 0.0f;
 #pragma unroll
                 for (int r = 0; r < kMaxParts; ++r) {
-                    m_[r] = r < parts ? peer_float(&s_part_m[head], r) : kNone;
-                    l_[r] = r < parts ? peer_float(&s_part_l[head], r) : 0.0f;
+                    ml[r] = r < parts ? peer_float4(&s_part_ml[head], r) : make_float4(kNone, 0.0f, 0.0f, 0.0f);
                     o_[r] = r < parts ? peer_float(&s_part[x], r) : 0.0f;
+                    m_[r] = {ml[r].x, ml[r].y};
                 }
-#pragma unroll
-                for (int r = 0; r < kMaxParts; ++r)
-                    M = fmaxf(M, m_[r]);
+                const Top M = highest(m_);
 #pragma unroll
                 for (int r = 0; r < kMaxParts; ++r) {
-                    const float f = ex2(m_[r] - M);
-                    L = fmaf(l_[r], f, L);
+                    const float f = ex2(Top{ml[r].x, ml[r].y}.over(M));
+                    L = fmaf(ml[r].z, f, L);
                     O = fmaf(o_[r], f, O);
                 }
                 store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
@@ -608,7 +654,8 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, 
     constexpr int kLanes = D / 4;                        // lanes of a row, four channels each
     constexpr int kRows = kThreads / kLanes;             // parts in flight per round
     __shared__ int64_t pre[RKV_MAX_BATCH + 1];
-    __shared__ float s_f[kMaxCtas], s_r[2][kWarps];
+    __shared__ float s_f[kMaxCtas], s_l[kWarps];
+    __shared__ float2 s_m[kWarps];
     __shared__ float4 s_o[kRows][kLanes];
     const int b = blockIdx.x, kvh = blockIdx.y / a.G, head = blockIdx.y % a.G, tid = threadIdx.x;
     tile_prefix(a, pre);
@@ -633,31 +680,38 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, 
         first[k] = i < np ? __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D) + col)
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    float M = kNone;
-    for (int i = tid; i < np; i += kThreads)
-        M = fmaxf(M, __ldcg(&a.part_ml[slot(i)]).x);
-    M = warp_max(M);
-    if ((tid & 31) == 0)
-        s_r[0][tid >> 5] = M;
-    __syncthreads();
+    Top M = kNoTop;
+    for (int i = tid; i < np; i += kThreads) {
+        const float4 ml = __ldcg(&a.part_ml[slot(i)]);
+        M.raise({ml.x, ml.y});
+    }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        M = fmaxf(M, s_r[0][w]);
+    for (int d = 16; d > 0; d >>= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, M.x, d), sv = __shfl_down_sync(0xffffffffu, M.s, d);
+        M.raise({x, sv});
+    }
+    if ((tid & 31) == 0)
+        s_m[tid >> 5] = make_float2(M.x, M.s);
+    __syncthreads();
+    M = {s_m[0].x, s_m[0].y};
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w)
+        M.raise({s_m[w].x, s_m[w].y});
     float L = 0.0f;
     for (int i = tid; i < np; i += kThreads) {
-        const float2 ml = __ldcg(&a.part_ml[slot(i)]);
-        const float f = ex2(ml.x - M);
+        const float4 ml = __ldcg(&a.part_ml[slot(i)]);
+        const float f = ex2(Top{ml.x, ml.y}.over(M));
         s_f[i] = f;
-        L = fmaf(ml.y, f, L);
+        L = fmaf(ml.z, f, L);
     }
     L = warp_sum(L);
     if ((tid & 31) == 0)
-        s_r[1][tid >> 5] = L;
+        s_l[tid >> 5] = L;
     __syncthreads();
     L = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-        L += s_r[1][w];
+        L += s_l[w];
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -770,7 +824,7 @@ int decode_ctas(const rkv_kv8_cache& c, int sms)
 uint64_t kv8_decode_ws_bytes(const rkv_kv8_cache& c, int sms)
 {
     const uint64_t G = c.n_q_heads / c.n_kv_heads;
-    return 2ull * decode_ctas(c, sms) * G * (c.head_dim * 4 + 8);
+    return 2ull * decode_ctas(c, sms) * G * (c.head_dim * 4 + 16);
 }
 
 cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32_t* table, const int32_t* lengths,
@@ -801,7 +855,7 @@ cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32
     const bool e4m3 = c.code_type == RKV_KV8_E4M3, f16 = c.in_dtype == RKV_DTYPE_F16;
     const int ctas = decode_ctas(c, sms);
     a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + 2ll * ctas * a.G * c.head_dim);
+    a.part_ml = reinterpret_cast<float4*>(a.part_o + 2ll * ctas * a.G * c.head_dim);
     const int parts = cluster_parts(c);
     return c.head_dim == 128 ? launch_d<128>(a, e4m3, f16, ctas, parts, st) : launch_d<64>(a, e4m3, f16, ctas, parts, st);
 }
