@@ -4,11 +4,14 @@
 //
 // The scales stay out of the products: with x_i = scale log2(e) sK_blk (q_g . codeK_i) the kernel keeps,
 // over the tokens seen so far, M = max_i (x_i + log2 sV_blk) and
-//   O = sum_i w_i codeV_i,  L = sum_i w_i / sV_blk,  w_i = 2^15 2^(x_i + log2 sV_blk - M) <= 2^15,
-// so out = O / L.  Folding the V scale into the exponent bounds every w_i whatever the blocks' scales, so
+//   L = sum_i t_i,  t_i = 2^15 2^(x_i - M),  O = sum_i w_i codeV_i,  w_i = t_i sV_blk <= 2^15,
+// so out = O / L.  Having the V scale in M bounds every w_i whatever the blocks' scales, so
 // it can enter the second product as a binary16 number (11 significant bits, rounded to nearest: the same
 // or finer than a 16-bit output); the factor 2^15 keeps the weights of a flat context of millions of tokens
-// out of binary16's subnormals.
+// out of binary16's subnormals.  A block whose V scale is 0 counts in M with the smallest scale, 2^-64, and has w_i = 0: it
+// neither lifts M over blocks of small scales nor is lost in L.  t_i lies within 2^79 and, for the largest logit,
+// above 2^-106; L is scaled by 2^(M - M') in two halves, which alone can fall below fp32's range (scales of 2^-64
+// beside 2^80) while the product with L does not.
 // M is kept as the two terms of the token that attains it (Top below), and the logits are subtracted from one
 // another before anything small is added: x_i + log2 sV_blk, or 15 - M, rounded to 32 bits would be off by 8 and more
 // for logits of 2^25 and beyond, past binary16's range and with equal logits weighted by their scales.
@@ -57,6 +60,7 @@ constexpr int kTile = 16 * kWarps;     // tokens per CTA step
 constexpr int kCtasPerSm = 4;          // at 128 registers; 4 requests of 131072 tokens: 183 us, three 191 us, two 246 us
 constexpr int kMaxCtas = 160 * kCtasPerSm;
 constexpr float kNone = -FLT_MAX;      // logit before any token
+constexpr float kZeroScale = -64.0f;   // log2 of the scale that a scale of 0 has in the maximum (kMinScale)
 constexpr float kWeightExp = 15.0f;    // weights are kept times 2^15: binary16 then holds 2^-39 .. 1 of the largest
 
 struct DecodeArgs {
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             const float sk = c.sk, sv = c.sv;
             c.load_k(a, id, next_row, kvh, lane);
             const bool in0 = live && tok + g < len, in1 = live && tok + g + 8 < len;
-            const float lsv = sv_ok ? __log2f(sv) : 0.0f, rsv = sv_ok ? __frcp_rn(sv) : 1.0f;
+            const float lsv = sv_ok ? __log2f(sv) : kZeroScale, wsv = sv_ok ? sv : 0.0f;
             uint32_t wf[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -503,13 +507,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                     top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 8));
                     top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 16));
                 }
-                float d0 = lsv - m[n][0].s, d1 = lsv - m[n][1].s;
-                const bool up0 = (top[0] - m[n][0].x) + d0 > 0.0f, up1 = (top[1] - m[n][1].x) + d1 > 0.0f;
+                const bool up0 = Top{top[0], lsv}.over(m[n][0]) > 0.0f, up1 = Top{top[1], lsv}.over(m[n][1]) > 0.0f;
                 if (__any_sync(0xffffffffu, up0 || up1)) {
                     const Top m0 = up0 ? Top{top[0], lsv} : m[n][0], m1 = up1 ? Top{top[1], lsv} : m[n][1];
-                    const float r0 = ex2(m[n][0].over(m0)), r1 = ex2(m[n][1].over(m1));
-                    l[n][0] *= r0;
-                    l[n][1] *= r1;
+                    float r0 = ex2(0.5f * m[n][0].over(m0)), r1 = ex2(0.5f * m[n][1].over(m1));
+                    l[n][0] = l[n][0] * r0 * r0;
+                    l[n][1] = l[n][1] * r1 * r1;
+                    r0 *= r0;
+                    r1 *= r1;
 #pragma unroll
                     for (int i = 0; i < kSteps; ++i) {
                         o[n][i][0] *= r0;
@@ -519,16 +524,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                     }
                     m[n][0] = m0;
                     m[n][1] = m1;
-                    d0 = lsv - m0.s;
-                    d1 = lsv - m1.s;
                 }
-                d0 += kWeightExp;
-                d1 += kWeightExp;
-                const float w00 = ex2((sc[n][0] - m[n][0].x) + d0), w01 = ex2((sc[n][1] - m[n][1].x) + d1);
-                const float w10 = ex2((sc[n][2] - m[n][0].x) + d0), w11 = ex2((sc[n][3] - m[n][1].x) + d1);
-                l[n][0] = fmaf(w00 + w10, rsv, l[n][0]);
-                l[n][1] = fmaf(w01 + w11, rsv, l[n][1]);
-                const __half2 p0 = __floats2half2_rn(w00, w01), p1 = __floats2half2_rn(w10, w11);
+                const float d0 = kWeightExp - m[n][0].s, d1 = kWeightExp - m[n][1].s;
+                const float t00 = ex2((sc[n][0] - m[n][0].x) + d0), t01 = ex2((sc[n][1] - m[n][1].x) + d1);
+                const float t10 = ex2((sc[n][2] - m[n][0].x) + d0), t11 = ex2((sc[n][3] - m[n][1].x) + d1);
+                l[n][0] += t00 + t10;
+                l[n][1] += t01 + t11;
+                const __half2 p0 = __floats2half2_rn(t00 * wsv, t01 * wsv), p1 = __floats2half2_rn(t10 * wsv, t11 * wsv);
                 wf[n][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
                 wf[n][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
             }
@@ -593,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
             float L = 0.0f, O = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(Top{ml[w].x, ml[w].y}.over(M));
-                L = fmaf(ml[w].z, f, L);
-                O = fmaf(s_o[w][head][ch], f, O);
+                const float f = ex2(0.5f * Top{ml[w].x, ml[w].y}.over(M));
+                L = fmaf(ml[w].z * f, f, L);
+                O = fmaf(s_o[w][head][ch], f * f, O);
             }
             if constexpr (kCluster) {
                 s_part[x] = O;
@@ -627,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) kv8_decode
                 const Top M = highest(m_);
 #pragma unroll
                 for (int r = 0; r < kMaxParts; ++r) {
-                    const float f = ex2(Top{ml[r].x, ml[r].y}.over(M));
-                    L = fmaf(ml[r].z, f, L);
-                    O = fmaf(o_[r], f, O);
+                    const float f = ex2(0.5f * Top{ml[r].x, ml[r].y}.over(M));
+                    L = fmaf(ml[r].z * f, f, L);
+                    O = fmaf(o_[r], f * f, O);
                 }
                 store_out(a.out, a.out_dtype, (static_cast<int64_t>(b) * a.Hq + kvh * a.G + head) * D + ch,
                           L != 0.0f ? O / L : 0.0f);
@@ -700,9 +702,9 @@ __global__ void __launch_bounds__(kThreads) kv8_join_kernel(const DecodeArgs a, 
     float L = 0.0f;
     for (int i = tid; i < np; i += kThreads) {
         const float4 ml = __ldcg(&a.part_ml[slot(i)]);
-        const float f = ex2(Top{ml.x, ml.y}.over(M));
-        s_f[i] = f;
-        L = fmaf(ml.z, f, L);
+        const float f = ex2(0.5f * Top{ml.x, ml.y}.over(M));
+        s_f[i] = f * f;
+        L = fmaf(ml.z * f, f, L);
     }
     L = warp_sum(L);
     if ((tid & 31) == 0)

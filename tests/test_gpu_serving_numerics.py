@@ -7,45 +7,66 @@ import torch
 
 import long_context_attention_rkv_b200 as rkv
 import serving_ref as ref
-from test_gpu_serving import CODE, ints, random_cache, side_rows
+from test_gpu_serving import cache_of, ints, offsets, values
 
 pytestmark = pytest.mark.gpu
 
 
 # --- decode over the 8-bit cache ----------------------------------------------------------------
 
-def widened(cache, table, tokens):
-    """The same cache behind table rows that could hold `tokens` tokens (the form with the workspace and the join)."""
-    c = cache.c
-    wide = torch.full((table.shape[0], -(-tokens // c.block_size)), -1, dtype=torch.int32)
-    wide[:, :table.shape[1]] = table
-    cfg = rkv.make_kv8_config(c.head_dim, c.n_kv_heads, c.n_q_heads, c.block_size, c.n_blocks, wide.shape[1], c.batch,
-                              c.code_type, c.in_dtype, c.out_dtype, c.scale)
-    return rkv.KV8Cache(cfg, cache.codes_K, cache.codes_V, cache.scale_K, cache.scale_V), wide
+def block_cache(gen, code, form, d, hq, hkv):
+    """Random codes in shuffled blocks of 16 tokens, fp32 out, in the two forms of the decode, several tiles of 64 tokens per CTA
+    in both: "clusters" (150 rows of at most 512 tokens) and "workspace" (5 requests of up to 30000 tokens)."""
+    lens = [512, 300, 1, 64, 65] * 30 if form == "clusters" else [30000, 17, 20000, 25001, 129]
+    need = [-(-n // 16) for n in lens]
+    n_blocks, width = sum(need), max(need)
+    cache = cache_of(code, d=d, hkv=hkv, hq=hq, block=16, n_blocks=n_blocks, max_blocks=width, batch=len(lens),
+                     out_dtype=rkv.RKV_DTYPE_F32)
+    ids = torch.randperm(n_blocks, generator=gen, dtype=torch.int32)
+    table = torch.zeros((len(lens), width), dtype=torch.int32)
+    for b, (k, lo) in enumerate(zip(need, offsets(need))):
+        table[b, :k] = ids[lo:lo + k]
+    for codes, scale in ((cache.codes_K, cache.scale_K), (cache.codes_V, cache.scale_V)):
+        x = torch.randn(codes.shape, generator=gen) * 30
+        codes.copy_((x.round() if code == "int8" else x).clamp(-127, 127).to(codes.dtype))
+        scale.copy_(torch.exp2((torch.rand(scale.shape, generator=gen) - 0.5) * 4.0) / 30)
+    return cache, table, lens
 
 
-def decode_both(cache, table, lens, q, check):
-    """By both forms: `check` on the output of each."""
-    odt = {v: k for k, v in CODE.items()}[cache.c.out_dtype]
-    for c, t in ((cache, table), widened(cache, table, 40000)):
-        out = torch.full(q.shape, 7.0, dtype=odt, device="cuda")
-        c.decode(q, t.cuda(), ints(lens), out)
-        assert c.device_error() == 0
-        check(out)
+def check_all(cache, table, lens, q, with_logits=True):
+    """Every request against the reference.  with_logits False: logits that are exact up to one rounding that equal ones
+    share, so their part of the bound is 0."""
+    out = torch.full(q.shape, 7.0, device="cuda")
+    cache.decode(q.cuda(), table.cuda(), ints(lens), out)
+    assert cache.device_error() == 0
+    got = out.double().cpu()
+    assert got.isfinite().all()
+    sides = [(c.cpu().float(), s.cpu().double()) for c, s in ((cache.codes_K, cache.scale_K), (cache.codes_V, cache.scale_V))]
+    qmax = 127.0 if cache.codes_V.dtype is torch.int8 else 448.0
+    for b, n in enumerate(lens):
+        ids = table[b, :-(-n // 16)].long()
+        k, v = ((c[ids].double() * s[ids][..., None, None]).transpose(1, 2).reshape(-1, c.shape[1], c.shape[3])[:n]
+                for c, s in sides)
+        want, _, mag, spread = ref.attention(q[b:b + 1], k, v, torch.ones((1, n), dtype=torch.bool))
+        floor = 2.0 ** -40 * qmax * float(sides[1][1][ids].max())
+        tol, _ = ref.bounds(want, mag, spread if with_logits else 0.0 * spread, q.shape[2], n, torch.float16, torch.float32,
+                            floor)
+        err = (got[b:b + 1] - want).abs()
+        assert (err <= tol).all(), f"request {b} of {n}: {float((err / tol).max())} times the bound"
 
 
+@pytest.mark.parametrize("form", ["clusters", "workspace"])
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 @pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 3, 1), (128, 24, 2)])
-@pytest.mark.parametrize("exponent", [12, 20, 23, 24, 25, 26, 27, 28, 30, 40, 70, 100])
-def test_decode_far_logits(code, d, hq, hkv, exponent):
+@pytest.mark.parametrize("exponent", [12, 20, 23, 24, 25, 27, 28, 40, 100])
+def test_decode_far_logits(form, code, d, hq, hkv, exponent):
     """One channel carries logits near +-2^exponent with odd significands, taken from three key codes, so the tokens of
     the largest logit share the weight, whatever their value scales; the others lie at least 2^(exponent - 5) below.
 
     A product of two codes is exact in 32 bits, so equal codes have equal logits and the logit part of the bound is
-    0: spread is 0 in it.  (At 2^12 the next code's weight is 2^-128 or less.)"""
+    0.  (At 2^12 the next code's weight is 2^-128 or less.)"""
     g = torch.Generator().manual_seed(exponent + hq)
-    lens = [700, 130, 1]
-    cache, table = random_cache(g, code, lens, d, hkv, hq, 16, torch.bfloat16, out_dtype=torch.float32)
+    cache, table, lens = block_cache(g, code, form, d, hq, hkv)
     pick = torch.tensor([64.0, 88.0, 104.0])[torch.randint(0, 3, tuple(cache.codes_K.shape[:3]), generator=g)]
     cache.codes_K.view(torch.uint8).zero_()
     cache.codes_K[..., 0] = pick.to(cache.codes_K.dtype).cuda()
@@ -54,17 +75,34 @@ def test_decode_far_logits(code, d, hq, hkv, exponent):
     top = 2.0 ** (exponent - exponent // 2) * math.sqrt(d) / 104 / 1.2345
     q = torch.zeros((len(lens), hq, d))
     q[..., 0] = top * (0.5 + torch.rand((len(lens), hq), generator=g)) * (torch.randint(0, 2, (len(lens), hq), generator=g) * 2 - 1)
-    q = q.to(torch.bfloat16).cuda()
+    check_all(cache, table, lens, q.to(torch.bfloat16), with_logits=False)
 
-    def check(out):
-        assert out.isfinite().all()
-        for b, n in enumerate(lens):
-            ids = table[b, :-(-n // 16)].long()
-            k, v = side_rows(cache.codes_K, cache.scale_K, ids, n), side_rows(cache.codes_V, cache.scale_V, ids, n)
-            want, _, mag, spread = ref.attention(q[b:b + 1].cpu(), k, v, torch.ones((1, n), dtype=torch.bool))
-            floor = 2.0 ** -40 * ref.QMAX[code] * float(cache.scale_V[ids.cuda()].max())
-            tol, _ = ref.bounds(want, mag, 0.0 * spread, d, n, torch.float16, torch.float32, floor)
-            err = (out[b:b + 1].double().cpu() - want).abs()
-            assert (err <= tol).all(), f"request {b}: {float((err / tol).max())} times the bound"
 
-    decode_both(cache, table, lens, q, check)
+@pytest.mark.parametrize("form", ["clusters", "workspace"])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("exponents", [[-64], [-40], [-30], [-8], [80], [-64, 80], [-40, 60, 0, -10]])
+@pytest.mark.parametrize("logits", ["equal", "spread", "zeros first", "zeros last"])
+def test_decode_zero_value_scales_beside_any_other(form, code, exponents, logits):
+    """Blocks whose value scale is 0 (values of 0, whatever their codes) among blocks with scales near 2^exponents: their
+    tokens count in the sum of the weights and nowhere else.  All logits 0, spread, or those of the zero blocks
+    the largest or the smallest by 2^5."""
+    g = torch.Generator().manual_seed(len(exponents) + exponents[0] + 100)
+    cache, table, lens = block_cache(g, code, form, 64, 6, 2)
+    n, hkv = cache.scale_V.shape
+    e = torch.tensor(exponents, dtype=torch.float32)[torch.randint(0, len(exponents), (n, hkv), generator=g)]
+    scale_V = torch.exp2(e) * (1 + torch.rand((n, hkv), generator=g))
+    zero = torch.rand((n, hkv), generator=g) < 0.2
+    zero[table[:, 0].long()] = torch.tensor([True, False])
+    scale_V[zero] = 0.0
+    cache.scale_V.copy_(scale_V)
+    q = values(g, (len(lens), 6, 64), torch.bfloat16)
+    if logits == "equal":
+        cache.scale_K.zero_()
+    if logits.startswith("zeros"):
+        codes = cache.codes_K.float()
+        codes[..., 0] = torch.where(zero, 64.0, -64.0)[..., None].cuda() * (1 if logits == "zeros first" else -1)
+        cache.codes_K.copy_(codes.to(cache.codes_K.dtype))
+        cache.scale_K.fill_(1 / 32)
+        q = q / 64
+        q[..., 0] = 64.0
+    check_all(cache, table, lens, q)
