@@ -20,7 +20,8 @@
 //     P V runs beside the next softmax, so neither product is waited for in the steady state;
 //   - one thread owns one row (TMEM lane): no shuffles, and the row's maximum and sum never leave registers;
 //   - the accumulator is only rescaled when a row's maximum grew by more than 2^8: rare after the first tiles, so
-//     almost no step waits for the product before it;
+//     almost no step waits for the product before it.  The maximum is kept as one of S, without the factor c, so that
+//     differences are exact; where c max is large the weights are formed from them too (kFar);
 //   - a share of the exponentials runs on the FMA pipes (exp2_pair below).
 //
 // Work split: items (sequence, pair of query tiles, kv-head) from those with many keys to those with few (Schedule
@@ -59,11 +60,14 @@ constexpr int kM = 128;                 // rows of a query tile (TMEM lanes)
 constexpr int kN = 64;                  // keys of a tile
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;     // query tile t: S at 128 t, P (two buffers) at 128 t + 64 and + 96, O at 256 + 128 t
-constexpr float kNone = -FLT_MAX;       // running maximum before any key
+constexpr float kNone = -FLT_MAX;       // running maximum (of S) before any key
 constexpr int kPoly = 8;                // every kPoly-th pair of exponentials goes to the FMA pipes (0: none); 8192
                                         // tokens: share 0 451 us, 6 % 445, 12 % 447, 25 % 467, 50 % 569 (issue-bound)
 constexpr float kLazy = 8.0f;           // the accumulator is rescaled when the maximum grows by 2^8: sums stay far below
                                         // fp32's range, binary16 weights (times 2^kBias) below 2^16
+constexpr float kFar = 65536.0f;        // maxima (in units of log 2) from which S - max is formed before the factor c: below, the
+                                        // roundings of c max and of the bias' sum with it move an exponent by at most 2^-7;
+                                        // from 2^24 on they would move it past binary16's range, from 2^31 past fp32's
 
 // Weights are kept times 2^kBias: binary16 then holds them up to 2^(8 + 7) and down to 2^-32 of the largest
 // (a flat row of a million keys stays clear of its smallest step); bf16 has fp32's range.
@@ -746,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lim = it.L - it.n + tok;              // last key that this row sees
             const bool valid = row < a.ntok * a.G && tok < it.n;
             const int n = max(nk, it.nk(1 - t)), jb = first_tile(n), je = end_tile(n), jt = min(nk, je);
-            float m = kNone;
+            float m = kNone;                                // of S: c m_i is the formula's maximum
             uint64_t sum = pair(0.0f, 0.0f);
             for (int j = jb; j < jt; ++j, ++c) {
                 wait(&bars->s_full[t], c & 1);
@@ -779,13 +783,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t1 = max3(t1, s[62], s[63]);
                 t0 = max3(t0, t1, t2);
                 // rows that are not stored take no part in what the warp decides together
-                const float top = valid ? max3(t0, t0, t3) * a.c : -INFINITY;
+                const float top = valid ? max3(t0, t0, t3) : -INFINITY;
                 // the accumulator keeps its old maximum until the new one is 2^8 larger (the first tile counts as such);
                 // a warp rescales together.  A NaN becomes the maximum, and with it every weight of its row
-                if (__any_sync(0xffffffffu, !(top <= m + kLazy))) {
+                if (__any_sync(0xffffffffu, !((top - m) * a.c <= kLazy))) {
                     const float was = m;
-                    m = top <= m + kLazy ? m : top;
-                    const float f = ex2(was - m);
+                    m = (top - m) * a.c <= kLazy ? m : top;
+                    const float f = ex2((was - m) * a.c);
                     // the product before this step still adds to O
                     if (j > jb)
                         wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
@@ -817,7 +821,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                 }
                 const uint32_t tm_p = tm_s + 64 + 32 * (c & 1);
-                const uint64_t cc = pair(a.c, a.c), off = pair(kBias<kF16> - m, kBias<kF16> - m);
+                // exponents s c + off; rows without a key so far keep a finite offset whatever c
+                float off1 = kBias<kF16> - fmaxf(m * a.c, kNone);
+                const bool far = m != kNone && !(fabsf(m * a.c) < kFar);
+                if (__any_sync(0xffffffffu, far)) {
+                    const float base = far ? m : 0.0f;
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        s[x] -= base;
+                    off1 = far ? kBias<kF16> : off1;
+                }
+                const uint64_t cc = pair(a.c, a.c), off = pair(off1, off1);
                 uint64_t a0 = pair(0.0f, 0.0f), a1 = a0;
                 named_sync(my_turn, 64);
 #pragma unroll
@@ -865,13 +879,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l0, l1;
             unpair(sum, l0, l1);
             const float l = l0 + l1, inv_l = sees ? 1.0f / l : 0.0f;
-            const float log_sum = sees ? (m - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            const float log_sum = sees ? (m * a.c - kBias<kF16> + log2f(l)) * 0.6931471805599453f : -INFINITY;
             if (jt > jb)
                 wait(&bars->pv_done[t][(c - 1) & 1], ((c - 1) >> 1) & 1);
             const bool store = ok && valid;
             if constexpr (kSplit) {
                 // The parts (m, l, O) of the cluster's CTAs go through the ring, which the item has left, and CTA `part` joins
-                // the columns from part * D / parts on: M = max m_x, f_x = 2^(m_x - M), O = sum f_x O_x / sum f_x l_x.
+                // the columns from part * D / parts on: M = max m_x, f_x = 2^(c (m_x - M)), O = sum f_x O_x / sum f_x l_x.
                 // Parts without a key tile are (lowest float, 0, 0).
                 if (r > 0)
                     wait(&bars->part_read, (r - 1) & 1);
@@ -906,12 +920,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     M = max3(M, M, ml[x].x);
 #pragma unroll
                 for (uint32_t x = 0; x < kMaxParts; ++x) {
-                    ml[x].x = ex2(ml[x].x - M);
+                    ml[x].x = ex2((ml[x].x - M) * a.c);
                     sum_l = fmaf(ml[x].x, ml[x].y, sum_l);
                 }
                 const float inv = sees ? 1.0f / sum_l : 0.0f;
                 if (store && a.lse && part == 0)
-                    a.lse[q_row * a.Hq + head] = sees ? (M - kBias<kF16> + log2f(sum_l)) * 0.6931471805599453f : -INFINITY;
+                    a.lse[q_row * a.Hq + head] = sees ? (M * a.c - kBias<kF16> + log2f(sum_l)) * 0.6931471805599453f : -INFINITY;
                 const int cols = D / static_cast<int>(parts);
 #pragma unroll 1
                 for (int col = part * cols; col < static_cast<int>(part + 1) * cols; col += 8) {

@@ -7,7 +7,7 @@ import torch
 
 import long_context_attention_rkv_b200 as rkv
 import serving_ref as ref
-from test_gpu_serving import cache_of, ints, offsets, values
+from test_gpu_serving import cache_of, check_prefill, ints, offsets, prefill, values
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,83 @@ def test_decode_zero_value_scales_beside_any_other(form, code, exponents, logits
         q = q / 64
         q[..., 0] = 64.0
     check_all(cache, table, lens, q)
+
+
+# --- prompt attention -------------------------------------------------------------------------
+
+FAR = [(torch.bfloat16, e) for e in (12, 15, 16, 17, 20, 22, 24, 26, 28, 31, 36, 60, 100)] + \
+      [(torch.float16, e) for e in (12, 15, 16, 17, 20, 22, 24, 26, 28)]
+
+
+def check_far(q, K, V, off, out, lse, spread, scale=None, kv_off=None):
+    kv_off = off if kv_off is None else kv_off
+    for b in range(len(off) - 1):
+        rows, keys = slice(off[b], off[b + 1]), slice(kv_off[b], kv_off[b + 1])
+        n, L = off[b + 1] - off[b], kv_off[b + 1] - kv_off[b]
+        allowed = torch.arange(L)[None] <= (L - n + torch.arange(n))[:, None]
+        want, wlse, mag, s = ref.attention(q[rows].cpu(), K[keys].cpu(), V[keys].cpu(), allowed, scale)
+        floor = 2.0 ** -32 * float(V[keys].abs().max()) if q.dtype is torch.float16 else 0.0
+        tol, ltol = ref.bounds(want, mag, spread + 0.0 * s, q.shape[2], L, q.dtype, out.dtype, floor)
+        got = out[rows].double().cpu()
+        assert got.isfinite().all(), f"sequence {b}"
+        assert ((got - want).abs() <= tol).all(), f"sequence {b}: {float(((got - want).abs() / tol).max())} times the bound"
+        assert ((lse[rows].double().cpu() - wlse).abs() <= ref.lse_bound(wlse, ltol)).all(), f"sequence {b}: log-sums"
+
+
+@pytest.mark.parametrize("dtype,exponent", FAR)
+@pytest.mark.parametrize("d,hq,hkv,new,keys", [(64, 4, 1, [300, 70], None), (128, 7, 1, [150], None),
+                                               (64, 8, 1, [3], [2000])])
+def test_prefill_far_logits(dtype, exponent, d, hq, hkv, new, keys):
+    """One channel carries logits near +-2^exponent with odd significands, three key values: the keys of the
+    largest logit share the weight, the others lie at least 2^(exponent - 5) below.  A product of two 16-bit
+    inputs is exact in 32 bits, so equal keys have equal logits and the logit part of the bound is 0.  Whole prompts,
+    and few rows over many keys (shared by a cluster)."""
+    g = torch.Generator().manual_seed(exponent + d)
+    off = offsets(new)
+    kv_off = off if keys is None else offsets(keys)
+    n, L = off[-1], kv_off[-1]
+    q, K = torch.zeros((n, hq, d)), torch.zeros((L, hkv, d))
+    half = 2.0 ** (exponent // 2)
+    K[..., 0] = half * torch.tensor([1.0, 1.375, 1.625])[torch.randint(0, 3, (L, hkv), generator=g)] * 1.0859375
+    top = 2.0 ** exponent * math.sqrt(d) / half / 1.765
+    scale = 0.0
+    if dtype is torch.float16:                     # the range of q: the scale carries the rest
+        scale = top / 8.0 / math.sqrt(d)
+        top = 8.0
+    q[..., 0] = top * (0.5 + torch.rand((n, hq), generator=g)) * (torch.randint(0, 2, (n, hq), generator=g) * 2 - 1)
+    q, K, V = q.to(dtype).cuda(), K.to(dtype).cuda(), values(g, (L, hkv, d), dtype).cuda()
+    out, lse = prefill(q, K, V, off, dict(out_dtype=rkv.RKV_DTYPE_F32, scale=scale), kv_off=None if keys is None else kv_off)
+    check_far(q, K, V, off, out, lse, 0.0, scale=float(torch.tensor(scale)) or None, kv_off=kv_off)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("bits", [10, 14, 17, 20, 22])
+@pytest.mark.parametrize("step", [3, 9, -4])
+def test_prefill_far_maximum_that_moves_slowly(dtype, sign, bits, step):
+    """Logits of sign 255 251 2^(bits - 16) / 2 and a second channel that adds whole numbers: the maximum grows by less than
+    2^8 from tile to tile (or falls).  All logits and their differences are exact in 32 bits (24 bits hold them), and the
+    weights that count lie within 60 of the largest: the rounding of 0.5 log2(e) moves an exponent by at most
+    60 2^-23, which spread = 1 covers ((d + 2) 2^-23)."""
+    n, d = 1000, 64
+    g = torch.Generator().manual_seed(bits)
+    q, K = torch.zeros((n, 2, d)), torch.zeros((n, 1, d))
+    q[..., 0], q[..., 1] = 255.0, 1.0
+    K[:, 0, 0] = sign * 251.0 * 2.0 ** (bits - 16)
+    K[:, 0, 1] = (torch.arange(n) // 64 * step).float()
+    q, K, V = q.to(dtype).cuda(), K.to(dtype).cuda(), values(g, (n, 1, d), dtype).cuda()
+    out, lse = prefill(q, K, V, [0, n], dict(out_dtype=rkv.RKV_DTYPE_F32, scale=0.5))
+    check_far(q, K, V, [0, n], out, lse, 1.0, scale=0.5)
+
+
+@pytest.mark.parametrize("scale", [4.0, 1e30, 1e-30])
+@pytest.mark.parametrize("keys", [468, 20, 449])
+def test_prefill_rows_that_see_nothing_of_their_first_tile(scale, keys):
+    """40 rows over few keys, each of a cluster's CTAs with one tile of 64 of them at most (the plane could hold 2000):
+    the last tile's CTA has rows that see none of it, and with 20 keys half of the rows see none at all.  With
+    factors whose product with the lowest maximum overflows, and a small one."""
+    g = torch.Generator().manual_seed(keys)
+    q, K, V = (values(g, (n, h, 64), torch.bfloat16).cuda() for n, h in ((40, 8), (2000, 1), (2000, 1)))
+    q = (q.float() * (0.1 if scale == 4.0 else 1.0 / scale)).to(torch.bfloat16)
+    out, lse = prefill(q, K, V, [0, 40], dict(scale=scale), kv_off=[0, 0], kv_len=[keys])
+    check_prefill(q, K, V, [0, 40], lambda b: (K[:keys], V[:keys]), out, lse, scale=float(torch.tensor(scale)))
