@@ -459,6 +459,12 @@ def _need(where: str, name: str, x, n: int, dtype, strided=False):
     _refuse(where, f"{name} must be {dtype}" + ("" if strided else ", contiguous") + f" and hold {n} elements")
 
 
+def _need_width(where: str, name: str, x, width: int):
+    """Refuses a tensor with rows of another width: the call steps over rows of `width` elements (a flat tensor has none)."""
+    if x.dim() > 1 and x.shape[-1] != width:
+        _refuse(where, f"{name} has rows of {x.shape[-1]} elements, not {width}")
+
+
 class Prefill:
     """Causal attention over packed prompts: a configuration and its device status word."""
 
@@ -597,10 +603,12 @@ class KV8Cache:
         i32 = self._i32
         if not (q.dtype is self._in and out.dtype is self._out and block_table.dtype is i32 and lengths.dtype is i32 and
                 q.numel() >= n and out.numel() >= n and block_table.numel() >= n_table and lengths.numel() >= n_len and
+                block_table.shape[-1] == self.c.max_blocks and
                 q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous() and lengths.is_contiguous()):
             _need("KV8Cache.decode", "q", q, n, self._in)
             _need("KV8Cache.decode", "out", out, n, self._out)
             _need("KV8Cache.decode", "block_table", block_table, n_table, i32)
+            _need_width("KV8Cache.decode", "block_table", block_table, self.c.max_blocks)
             _need("KV8Cache.decode", "lengths", lengths, n_len, i32)
         self._here("KV8Cache.decode")
         rkv_kv8_decode_attn(self.c, q, block_table, lengths, out, self.workspace, self.workspace.numel(), stream)

@@ -279,6 +279,20 @@ def test_cache_class_refuses_buffers_and_tensors(recorded, monkeypatch):
     refused(cache.decode, q, table, lens, q)
 
 
+def test_cache_class_refuses_tables_of_another_width(recorded):
+    # rows of a table made for longer requests: every request after the first would be read from the wrong place
+    cfg = rkv.make_kv8_config(head_dim=64, n_kv_heads=2, n_q_heads=4, block_size=16, n_blocks=6, max_blocks=3, batch=2)
+    cache, i32 = rkv.KV8Cache(cfg, device="cpu"), torch.int32
+    q, lens = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=i32)
+    for shape in ((2, 4), (3, 2), (6, 1), (2, 30), (1, 3, 4)):
+        refused(cache.decode, q, torch.zeros(shape, dtype=i32), lens, q.clone())
+    refused(cache.decode, q, rkv.BlockTables(2, 5, 16, 6, device="cpu").table, lens, q.clone())
+    assert not recorded
+    for shape in ((2, 3), (5, 3), (1, 2, 3), (6,)):        # rows behind the last request are not read
+        cache.decode(q, torch.zeros(shape, dtype=i32), lens, q.clone())
+    assert len(recorded) == 4
+
+
 def test_raw_calls_refuse_tensors_of_another_device(monkeypatch):
     monkeypatch.setattr(rkv, "_device", lambda: 0)
     x = torch.zeros(4, dtype=torch.int32)                            # on the CPU
