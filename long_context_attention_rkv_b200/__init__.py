@@ -465,6 +465,12 @@ def _need_width(where: str, name: str, x, width: int):
         _refuse(where, f"{name} has rows of {x.shape[-1]} elements, not {width}")
 
 
+def _need_heads(where: str, name: str, x, heads):
+    """The same for rows of heads = (heads, channels), which may be one dimension or two."""
+    if x.dim() > 2 and x.shape[-2:] != heads or x.dim() == 2 and x.shape[1] not in (heads[0] * heads[1], heads[1]):
+        _refuse(where, f"{name} has rows of {tuple(x.shape[1:])} elements, not {heads}")
+
+
 class Prefill:
     """Causal attention over packed prompts: a configuration and its device status word."""
 
@@ -506,6 +512,7 @@ class Prefill:
             _need("Prefill.attend", "kv_len", kv_len, n_len, self._i32)
         if lse is not None:
             _need("Prefill.attend", "lse", lse, n_lse, self._f32)
+            _need_width("Prefill.attend", "lse", lse, self.cfg.n_q_heads)
         rkv_prefill_attn(self.cfg, q, K, V, q_off, kv_off, kv_len, out, lse, self.status, stream)
 
     def device_error(self) -> int:
@@ -578,6 +585,7 @@ class KV8Cache:
                                                    self.status))
         self._in, self._out, self._i32 = _torch_dtype(cfg.in_dtype), _torch_dtype(cfg.out_dtype), torch.int32
         self._row = (cfg.n_kv_heads, cfg.head_dim)
+        self._heads, self._width = (cfg.n_q_heads, cfg.head_dim), cfg.max_blocks
         self._sizes = (cfg.batch * cfg.n_q_heads * cfg.head_dim, cfg.batch * cfg.max_blocks, cfg.batch)
         self.c = rkv_kv8_cache.from_buffer_copy(cfg)
         for name in ("codes_K", "codes_V", "scale_K", "scale_V"):
@@ -603,13 +611,15 @@ class KV8Cache:
         i32 = self._i32
         if not (q.dtype is self._in and out.dtype is self._out and block_table.dtype is i32 and lengths.dtype is i32 and
                 q.numel() >= n and out.numel() >= n and block_table.numel() >= n_table and lengths.numel() >= n_len and
-                block_table.shape[-1] == self.c.max_blocks and
+                block_table.shape[-1] == self._width and q.shape[1:] == self._heads and out.shape[1:] == self._heads and
                 q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous() and lengths.is_contiguous()):
             _need("KV8Cache.decode", "q", q, n, self._in)
             _need("KV8Cache.decode", "out", out, n, self._out)
             _need("KV8Cache.decode", "block_table", block_table, n_table, i32)
-            _need_width("KV8Cache.decode", "block_table", block_table, self.c.max_blocks)
+            _need_width("KV8Cache.decode", "block_table", block_table, self._width)
             _need("KV8Cache.decode", "lengths", lengths, n_len, i32)
+            _need_heads("KV8Cache.decode", "q", q, self._heads)
+            _need_heads("KV8Cache.decode", "out", out, self._heads)
         self._here("KV8Cache.decode")
         rkv_kv8_decode_attn(self.c, q, block_table, lengths, out, self.workspace, self.workspace.numel(), stream)
 

@@ -293,6 +293,25 @@ def test_cache_class_refuses_tables_of_another_width(recorded):
     assert len(recorded) == 4
 
 
+def test_classes_refuse_rows_of_other_heads(recorded):
+    cfg = rkv.make_kv8_config(head_dim=64, n_kv_heads=2, n_q_heads=4, block_size=16, n_blocks=6, max_blocks=3, batch=2)
+    cache, i32, bf = rkv.KV8Cache(cfg, device="cpu"), torch.int32, torch.bfloat16
+    table, lens, good = torch.zeros(2, 3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(2, 4, 64, dtype=bf)
+    for shape in ((2, 8, 64), (4, 2, 64), (2, 4, 128), (2, 512), (1, 4, 2, 64)):
+        refused(cache.decode, torch.zeros(shape, dtype=bf), table, lens, good.clone())
+        refused(cache.decode, good, table, lens, torch.zeros(shape, dtype=bf))
+    op = rkv.Prefill(rkv.make_prefill_config(64, 2, 4, 2, 10, 12), device="cpu")
+    q, K, off = torch.zeros(10, 4, 64, dtype=bf), torch.zeros(12, 2, 64, dtype=bf), torch.zeros(3, dtype=i32)
+    for shape in ((10, 8), (20, 2), (5, 10)):
+        refused(op.attend, q, K, K, off, q.clone(), lse=torch.zeros(shape))
+    assert not recorded
+    for shape in ((2, 4, 64), (3, 4, 64), (2, 256), (8, 64), (512,), (2, 1, 4, 64)):
+        cache.decode(torch.zeros(shape, dtype=bf), table, lens, torch.zeros(shape, dtype=bf))
+    for shape in ((10, 4), (12, 4), (40,)):
+        op.attend(q, K, K, off, q.clone(), lse=torch.zeros(shape))
+    assert len(recorded) == 9
+
+
 def test_raw_calls_refuse_tensors_of_another_device(monkeypatch):
     monkeypatch.setattr(rkv, "_device", lambda: 0)
     x = torch.zeros(4, dtype=torch.int32)                            # on the CPU
