@@ -595,8 +595,12 @@ class KV8Cache:
     def store(self, K_new, V_new, slot_map, stream=None):
         """K_new, V_new: [rows, kv_heads, head_dim] with the same row and head strides and contiguous channels;
         slot_map: int32 [rows] (negative: the row is skipped)."""
-        where, shape, strides = "KV8Cache.store", K_new.shape, K_new.stride()
-        if len(shape) != 3 or shape[1:] != self._row or V_new.shape != shape or V_new.stride() != strides or \
+        where, shape, strides, v_strides = "KV8Cache.store", K_new.shape, K_new.stride(), V_new.stride()
+        if len(shape) == 3 and (shape[0] == 1 or shape[1] == 1):       # a dimension of one has no step
+            heads, d = self._row
+            strides, v_strides = ((s[0] if shape[0] > 1 else heads * d, s[1] if shape[1] > 1 else d, *s[2:])
+                                  for s in (strides, v_strides)) if V_new.shape == shape else (strides, None)
+        if len(shape) != 3 or shape[1:] != self._row or V_new.shape != shape or v_strides != strides or \
                 strides[2] != 1 or K_new.dtype is not self._in or V_new.dtype is not self._in:
             _refuse(where, f"K_new and V_new must be {self._in} [rows, {self._row[0]}, {self._row[1]}] with equal strides "
                            "and contiguous channels")

@@ -312,6 +312,28 @@ def test_classes_refuse_rows_of_other_heads(recorded):
     assert len(recorded) == 9
 
 
+def test_store_class_takes_dimensions_of_one_with_any_stride(recorded):
+    # one new token, or one kv-head: the stride of a dimension of one says nothing about the layout
+    bf = torch.bfloat16
+    shape = dict(head_dim=64, block_size=16, n_blocks=6, max_blocks=3, batch=2)
+    two = rkv.KV8Cache(rkv.make_kv8_config(n_kv_heads=2, n_q_heads=4, **shape), device="cpu")
+    K, V = torch.zeros(1, 2, 64, dtype=bf), torch.zeros(1, 8, 64, dtype=bf)[:, 4:6]
+    slot = torch.zeros(5, dtype=torch.int32)
+    two.store(K, V, slot)
+    two.store(V, K, slot)
+    two.store(torch.as_strided(K, (1, 2, 64), (3, 64, 1)), V, slot)
+    one = rkv.KV8Cache(rkv.make_kv8_config(n_kv_heads=1, n_q_heads=4, **shape), device="cpu")
+    rows = torch.zeros(5, 64, dtype=bf)
+    one.store(rows.unsqueeze(1), rows.view(1, 5, 64).transpose(0, 1), slot)
+    one.store(torch.as_strided(rows, (5, 1, 64), (64, 1, 1)), rows.unsqueeze(1), slot)
+    one.store(rows[:1].unsqueeze(1), torch.as_strided(rows, (1, 1, 64), (5, 7, 1)), slot)
+    assert [a[3:5] for _, a in recorded] == [(128, 64)] * 3 + [(64, 64)] * 3
+    refused(one.store, rows.unsqueeze(1), torch.zeros(10, 64, dtype=bf)[::2].unsqueeze(1), slot)
+    refused(two.store, K, torch.zeros(1, 2, 128, dtype=bf)[..., :64], slot)
+    refused(two.store, K, torch.zeros(1, 3, 64, dtype=bf), slot)
+    refused(two.store, K, torch.zeros(2, 64, dtype=bf), slot)
+
+
 def test_raw_calls_refuse_tensors_of_another_device(monkeypatch):
     monkeypatch.setattr(rkv, "_device", lambda: 0)
     x = torch.zeros(4, dtype=torch.int32)                            # on the CPU
