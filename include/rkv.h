@@ -443,7 +443,7 @@ RKV_API rkv_status rkv_selftest_wait_timeout(int32_t* err_dev, void* stream);
  *   kv_padded       0: the rows of K and V of all sequences lie in one plane of kv_rows rows
  *                   (packed).  1: sequence b has a plane of kv_rows rows of its own, `kv_plane_stride`
  *                   apart (the layout that rkv_build_refs and rkv_compress read)
- *   scale           factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, finite
+ *   scale           factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, at most 2^127
  *   q_rows          rows of q, out and lse;  kv_rows  rows of a plane of K and V
  *   *_stride        element strides: of a row (token), of a head, of a plane.  Those of q, K and V are
  *                   multiples of 8 and rows of one head are head_dim contiguous elements; out_*
@@ -562,7 +562,7 @@ RKV_API rkv_status rkv_blocks_release(const rkv_blocks_config* cfg, const int32_
  *   in_dtype     RKV_DTYPE_BF16 or RKV_DTYPE_F16: K, V and q;  out_dtype  in_dtype or RKV_DTYPE_F32
  *   n_q_heads    a multiple of n_kv_heads, at most 16 times as many
  *   batch, max_blocks, block_size, n_blocks  as rkv_blocks_config
- *   scale        factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, finite
+ *   scale        factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, at most 2^127
  */
 #define RKV_KV8_INT8 0
 #define RKV_KV8_E4M3 1

@@ -2,7 +2,6 @@
 // Every entry point returns an rkv_status and never throws; see include/rkv.h.
 #include <atomic>
 #include <climits>
-#include <cmath>
 
 #include "api_common.h"
 #include "launchers.h"
@@ -42,7 +41,8 @@ constexpr int kMaxSms = 160;
 
 bool half_type(int32_t t) { return t == RKV_DTYPE_BF16 || t == RKV_DTYPE_F16; }
 
-bool scale_ok(float s) { return s == 0.0f || (s > 0.0f && std::isfinite(s)); }
+// Up to 2^127, so that its product with log2(e) is finite too.
+bool scale_ok(float s) { return s == 0.0f || (s > 0.0f && s <= 0x1p127f); }
 
 // Element strides below 2^38, so that byte strides fit a tensor map's 40 bits.
 bool stride_ok(int64_t s, int64_t unit) { return s > 0 && s % unit == 0 && s < (int64_t(1) << 38); }

@@ -194,6 +194,19 @@ def test_decode_refuses_pointers_and_short_workspaces():
         rkv.rkv_kv8_workspace(kv8_cfg(head_dim=32))
 
 
+@pytest.mark.parametrize("call,cfg", [(prefill_status, prefill_cfg), (store_status, kv8_cfg), (decode_status, kv8_cfg)])
+def test_scales_whose_product_with_log2e_overflows_are_refused(call, cfg):
+    for scale in (2.0 ** 127 * (1 + 2.0 ** -23), 3.4e38):
+        assert call(cfg(scale=scale)) == INVALID
+    largest = dict(scale=2.0 ** 127)
+    if call is prefill_status:
+        assert call(cfg(q_rows=0, **largest)) == 0
+    elif call is store_status:
+        assert call(cfg(**largest), n_rows=0) == 0
+    else:
+        assert call(cfg(**largest), bytes=0) == WORKSPACE          # the next check
+
+
 # --- the classes -----------------------------------------------------------------------------
 
 @pytest.fixture
