@@ -489,7 +489,9 @@ typedef struct rkv_prefill_config {
  *            bounded wait that ran out records RKV_ERR_TIMEOUT
  * Rows of K and V outside a sequence's keys may hold anything (NaN too) and do not reach it, but a
  * plane's kv_rows rows must be readable.  Inside a sequence a NaN key reaches the rows that see it and no
- * others; a non-finite value may reach earlier rows of the same 64 keys too.  q, K, V 16-byte aligned.  q, K, V must not overlap out or lse.
+ * others.  A value (of V) that is infinite or NaN may reach, besides the rows that see it, rows up to 128 / G + 14 before
+ * the first of these, G = n_q_heads / n_kv_heads (rows of one tile share a product, in which masked values meet weights
+ * of 0).  q, K, V 16-byte aligned; they must not overlap out or lse.
  * Softmax statistics and sums are 32-bit; the weights enter the second product in in_dtype.  No
  * workspace; calls on any streams may overlap.
  */

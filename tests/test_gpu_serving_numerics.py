@@ -186,3 +186,32 @@ def test_prefill_rows_that_see_nothing_of_their_first_tile(scale, keys):
     q = (q.float() * (0.1 if scale == 4.0 else 1.0 / scale)).to(torch.bfloat16)
     out, lse = prefill(q, K, V, [0, 40], dict(scale=scale), kv_off=[0, 0], kv_len=[keys])
     check_prefill(q, K, V, [0, 40], lambda b: (K[:keys], V[:keys]), out, lse, scale=float(torch.tensor(scale)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hq,hkv,prefix", [(2, 2, 0), (4, 2, 9), (7, 1, 0), (16, 1, 130)])
+def test_prefill_infinite_values_reach_no_further_than_said(dtype, hq, hkv, prefix):
+    """An infinite or NaN value at a key: rows more than 128 / G + 14 before the first that sees it, other
+    sequences and other channels are as without it; the rows that see it are not finite in its channel."""
+    g = torch.Generator().manual_seed(hq)
+    n, d, copies = 260, 64, 24
+    L, group = n + prefix, hq // hkv
+    q, K, V = (values(g, (m, h, d), dtype).cuda() for m, h in ((n, hq), (L, hkv), (L, hkv)))
+    off, kv_off = [n * i for i in range(copies + 1)], [L * i for i in range(copies + 1)]
+    clean, _ = prefill(q, K, V, [0, n], kv_off=[0, L])
+    at = [prefix + 11 * i for i in range(copies)]
+    V2 = V.repeat(copies, 1, 1)
+    for i, key in enumerate(at[:-1]):                                # the last sequence stays clean
+        V2[i * L + key, :, 5] = (math.inf, -math.inf, math.nan)[i % 3]
+    out, lse = prefill(q.repeat(copies, 1, 1), K.repeat(copies, 1, 1), V2, off, kv_off=kv_off)
+    assert lse.isfinite().all()
+    for i, key in enumerate(at):
+        rows, first = out[n * i:n * (i + 1)], key - prefix
+        others = torch.arange(d) != 5
+        assert torch.equal(rows[..., others], clean[..., others])
+        if i == copies - 1:
+            assert torch.equal(rows, clean)
+            continue
+        assert not rows[first:, :, 5].isfinite().any()
+        far = max(0, first - (128 // group + 14))
+        assert torch.equal(rows[:far], clean[:far]), (i, key)
