@@ -1,13 +1,14 @@
 """GPU parity of the serving operators where 32-bit logits, weights of few bits and scales of any size meet: what
 rounding must not turn into infinities, zeros or another mean."""
 import math
+import random
 
 import pytest
 import torch
 
 import long_context_attention_rkv_b200 as rkv
 import serving_ref as ref
-from test_gpu_serving import cache_of, check_prefill, ints, offsets, prefill, values
+from test_gpu_serving import cache_of, check_prefill, ints, offsets, prefill, same_cache, values
 
 pytestmark = pytest.mark.gpu
 
@@ -215,3 +216,51 @@ def test_prefill_infinite_values_reach_no_further_than_said(dtype, hq, hkv, pref
         assert not rows[first:, :, 5].isfinite().any()
         far = max(0, first - (128 // group + 14))
         assert torch.equal(rows[:far], clean[:far]), (i, key)
+
+
+# --- the 8-bit store --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,hkv,block,batch,rows,dtype", [
+    # sizes at which the writer's windows of rows are 16, 16, 32, 64, 64, 128 and 128 long
+    (64, 8, 16, 1, 700, torch.bfloat16), (128, 8, 16, 3, 1300, torch.float16), (64, 8, 32, 2, 1300, torch.float16),
+    (128, 8, 64, 1, 2500, torch.bfloat16), (64, 12, 64, 2, 1700, torch.bfloat16), (64, 8, 128, 2, 5200, torch.float16),
+    (128, 16, 128, 3, 2700, torch.bfloat16)])
+def test_store_windows_of_many_runs(code, d, hkv, block, batch, rows, dtype):
+    """Calls of many rows, bit for bit: runs that go on in a block from its middle, whole blocks, single tokens by the dozen
+    (many runs in a window), skipped rows between them, runs over a window's end; sizes that grow and fall between runs, so
+    scales grow in blocks that hold codes."""
+    r = random.Random(rows + block)
+    g = torch.Generator().manual_seed(rows)
+    n_blocks = 3 * rows // block + 400
+    cfg = rkv.make_kv8_config(d, hkv, hkv, block, n_blocks, n_blocks, batch, rkv.RKV_KV8_INT8 if code == "int8" else
+                              rkv.RKV_KV8_E4M3, rkv.RKV_DTYPE_BF16 if dtype is torch.bfloat16 else rkv.RKV_DTYPE_F16)
+    cache = rkv.KV8Cache(cfg)
+    rk, rv = (ref.Store(n_blocks, hkv, block, d, code) for _ in range(2))
+    held = [0] * n_blocks
+    for call in range(3):
+        slots, sizes = [], []
+        free = [b for b in range(n_blocks) if held[b] < block]
+        r.shuffle(free)
+        while len(slots) < rows:
+            kind = r.choice(["gap", "whole", "whole", "whole", "some", "singles"])
+            if kind == "gap":
+                m = r.randint(1, 40)
+                slots += [r.choice([-1, -7])] * m
+                sizes += [1.0] * m
+                continue
+            for _ in range(r.randint(1, 24) if kind == "singles" else 1):
+                b = free.pop()
+                m = 1 if kind == "singles" else block - held[b] if kind == "whole" else r.randint(1, block - held[b])
+                slots += range(b * block + held[b], b * block + held[b] + m)
+                sizes += [r.choice([0.02, 1.0, 1.0, 30.0])] * m
+                held[b] += m
+        for b in range(n_blocks):                      # the last run may have passed the end: keep what the call holds
+            held[b] -= sum(b * block <= s < (b + 1) * block for s in slots[rows:])
+        slots, sizes = slots[:rows], torch.tensor(sizes[:rows])[:, None, None]
+        K, V = ((values(g, (rows, hkv, d), torch.float32) * sizes).to(dtype) for _ in range(2))
+        cache.store(K.cuda(), V.cuda(), ints(slots))
+        rk.put(K, slots)
+        rv.put(V, slots)
+        assert cache.device_error() == 0
+        same_cache(cache, rk, rv)
