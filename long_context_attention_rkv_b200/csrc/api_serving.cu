@@ -211,7 +211,7 @@ rkv_status rkv_kv8_store(const rkv_kv8_cache* cache, const void* K_new, const vo
     s = device_sms(&sms);
     if (s != RKV_OK)
         return s;
-    return cuda_status(launch_kv8_store(*cache, K_new, V_new, row_stride, head_stride, slot_map, n_rows,
+    return cuda_status(launch_kv8_store(*cache, K_new, V_new, row_stride, head_stride, slot_map, n_rows, sms,
                                         static_cast<cudaStream_t>(stream)));
 }
 

@@ -799,12 +799,12 @@ cudaError_t launch_d(const DecodeArgs& a, bool e4m3, bool f16, int ctas, int par
 // and in clusters of 1 / 2 / 4 / 8: 1 request of 512 tokens 6.7 and 10.5 / 7.2 / 5.5 / 5.0 us, of 2049 8.6 and 27 / 15.6 /
 // 10.1 / 7.5, of 8192 13.2 and 90 / 47 / 26 / 15.2; 8 of 2049 15.6 and 27 / 16.1 / 11.8 / 11.6; 64 of 1024 38.1 and 32.3 /
 // 35.5 / 43 / 61, of 2049 61 and 56 / 59 / 67 / 85.  It also saves the host a launch (2 us).
-int cluster_parts(const rkv_kv8_cache& c)
+int cluster_parts(const rkv_kv8_cache& c, int sms)
 {
     constexpr int64_t kTiles = 8;
     const int64_t units = static_cast<int64_t>(c.batch) * c.n_kv_heads;
     const int64_t tiles = (static_cast<int64_t>(c.max_blocks) * c.block_size + kTile - 1) / kTile;
-    const int64_t at_once = 148 * (c.n_q_heads / c.n_kv_heads <= 8 ? kCtasPerSm : 2);
+    const int64_t at_once = static_cast<int64_t>(sms) * (c.n_q_heads / c.n_kv_heads <= 8 ? kCtasPerSm : 2);
     int parts = 1;
     while (parts < kMaxParts && (tiles > kTiles * parts || units * 2 * parts <= at_once))
         parts *= 2;
@@ -858,7 +858,7 @@ cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32
     const int ctas = decode_ctas(c, sms);
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float4*>(a.part_o + 2ll * ctas * a.G * c.head_dim);
-    const int parts = cluster_parts(c);
+    const int parts = cluster_parts(c, sms);
     return c.head_dim == 128 ? launch_d<128>(a, e4m3, f16, ctas, parts, st) : launch_d<64>(a, e4m3, f16, ctas, parts, st);
 }
 

@@ -391,13 +391,13 @@ cudaError_t launch_t(const StoreArgs& a, bool f16, dim3 grid, cudaStream_t st)
 // of 1 / 4 / 16 / 64 rows: 64 requests with 1 token each 4.6 us, in windows of 64 66 us; with 4 to 8 9.8 / 6.3 / 7.0 /
 // 16.8 us; with 12 to 24 20.6 / 9.9 / 7.0 / 9.5 us; 4 with 100 to 200 10.8 / 6.0 / 4.4 / 6.7 us; 1 with 32768 411 us in
 // windows of 1, 39.4 us in windows of 64.
-int window_of(int64_t n_rows, const rkv_kv8_cache& c)
+int window_of(int64_t n_rows, const rkv_kv8_cache& c, int sms)
 {
-    constexpr int64_t kManyCtas = 4 * 148;
+    const int64_t many_ctas = 4ll * sms;
     int w = 1;
     while (2 * w <= c.block_size && 2ll * w * c.batch <= n_rows)
         w *= 2;
-    while (w > 1 && 2ll * c.n_kv_heads * ((n_rows + w - 1) / w) < kManyCtas)
+    while (w > 1 && 2ll * c.n_kv_heads * ((n_rows + w - 1) / w) < many_ctas)
         w /= 2;
     return w;
 }
@@ -405,7 +405,7 @@ int window_of(int64_t n_rows, const rkv_kv8_cache& c)
 }  // namespace
 
 cudaError_t launch_kv8_store(const rkv_kv8_cache& c, const void* K_new, const void* V_new, int64_t row_stride,
-                             int64_t head_stride, const int32_t* slots, int64_t n_rows, cudaStream_t st)
+                             int64_t head_stride, const int32_t* slots, int64_t n_rows, int sms, cudaStream_t st)
 {
     StoreArgs a;
     a.Hkv = c.n_kv_heads;
@@ -413,7 +413,7 @@ cudaError_t launch_kv8_store(const rkv_kv8_cache& c, const void* K_new, const vo
     while ((1 << a.shift) < c.block_size)
         ++a.shift;
     a.n_blocks = c.n_blocks;
-    a.window = window_of(n_rows, c);
+    a.window = window_of(n_rows, c, sms);
     a.row_stride = row_stride;
     a.head_stride = head_stride;
     a.n_rows = n_rows;

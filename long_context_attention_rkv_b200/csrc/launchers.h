@@ -77,7 +77,7 @@ cudaError_t launch_blocks_release(const rkv_blocks_config& c, const int32_t* len
                                   const int32_t* table, int32_t* free_list, const int32_t* n_free,
                                   int32_t* lengths_out, int32_t* n_free_out, int32_t* err, cudaStream_t st);
 cudaError_t launch_kv8_store(const rkv_kv8_cache& c, const void* K_new, const void* V_new, int64_t row_stride,
-                             int64_t head_stride, const int32_t* slots, int64_t n_rows, cudaStream_t st);
+                             int64_t head_stride, const int32_t* slots, int64_t n_rows, int sms, cudaStream_t st);
 uint64_t kv8_decode_ws_bytes(const rkv_kv8_cache& c, int sms);
 cudaError_t launch_kv8_decode(const rkv_kv8_cache& c, const void* q, const int32_t* table, const int32_t* lengths,
                               void* out, void* workspace, int sms, cudaStream_t st);
