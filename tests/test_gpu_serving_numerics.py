@@ -36,7 +36,11 @@ def block_cache(gen, code, form, d, hq, hkv):
 
 def check_all(cache, table, lens, q, with_logits=True):
     """Every request against the reference.  with_logits False: logits that are exact up to one rounding that equal ones
-    share, so their part of the bound is 0."""
+    share, so their part of the bound is 0.
+
+    The floor of the bound (weights below binary16's normal range) also holds where a block of scale 0 sets the running
+    maximum, with the smallest scale 2^-64, and all other weights are small: the sum of the weights is 2^15 2^64 or more there, so
+    steps of 2^-25 times codes move the quotient by keys 2^-104 qmax at most, and no scale but 0 is below 2^-64."""
     out = torch.full(q.shape, 7.0, device="cuda")
     cache.decode(q.cuda(), table.cuda(), ints(lens), out)
     assert cache.device_error() == 0
