@@ -506,7 +506,7 @@ RKV_API rkv_status rkv_prefill_attn(const rkv_prefill_config* cfg, const void* q
  * Free blocks are a stack on the device: free_list[0 .. n_free - 1], the top last.  These two calls
  * keep the tables, on the device and without the host knowing a length.
  *   batch       requests, 1..RKV_MAX_BATCH
- *   max_blocks  entries of a table row
+ *   max_blocks  entries of a table row; max_blocks * block_size < 2^31
  *   block_size  tokens per block: 16, 32, 64 or 128
  *   n_blocks    blocks of the pool = capacity of free_list; n_blocks * block_size < 2^31
  */
@@ -563,7 +563,7 @@ RKV_API rkv_status rkv_blocks_release(const rkv_blocks_config* cfg, const int32_
  *                bits, largest 448.  qmax is 127 or 448
  *   in_dtype     RKV_DTYPE_BF16 or RKV_DTYPE_F16: K, V and q;  out_dtype  in_dtype or RKV_DTYPE_F32
  *   n_q_heads    a multiple of n_kv_heads, at most 16 times as many
- *   batch, max_blocks, block_size, n_blocks  as rkv_blocks_config
+ *   batch, max_blocks, block_size, n_blocks  as rkv_blocks_config; max_blocks * block_size at most 2^31 - 64
  *   scale        factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, at most 2^127
  */
 #define RKV_KV8_INT8 0

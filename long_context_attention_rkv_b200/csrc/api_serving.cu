@@ -99,6 +99,9 @@ rkv_status check_kv8(const rkv_kv8_cache* c)
         s = check_blocks(c->batch, c->max_blocks, c->block_size, c->n_blocks);
     if (s != RKV_OK)
         return s;
+    // the decode rounds lengths up to tiles of 64 tokens in 31 bits
+    if (static_cast<int64_t>(c->max_blocks) * c->block_size > INT32_MAX - 63)
+        return RKV_ERR_UNSUPPORTED;
     if (c->in_dtype == RKV_DTYPE_F32)
         return RKV_ERR_UNSUPPORTED;
     if (!half_type(c->in_dtype) || (c->out_dtype != c->in_dtype && c->out_dtype != RKV_DTYPE_F32) ||

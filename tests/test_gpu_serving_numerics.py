@@ -113,6 +113,35 @@ def test_decode_zero_value_scales_beside_any_other(form, code, exponents, logits
     check_all(cache, table, lens, q)
 
 
+
+def test_decode_lengths_next_to_31_bits():
+    """A length that the row cannot hold is clamped to the row, here the longest there is: 2^31 - 64 tokens, 2^27 - 4 times
+    the same block: their mean is that block's.
+
+    At most 2^31 / 64 / (148 * 4) + 1 = 56680 equal terms are added one after the other, in the numerator and in
+    the sum, each with an error of 2^-24 of the total, then 10 merges; weights and logits as in the other bounds."""
+    d, block = 64, 16
+    n_blocks, width = 3, 2 ** 27 - 4
+    g = torch.Generator().manual_seed(1)
+    cache = cache_of("int8", d=d, hkv=1, hq=2, block=block, n_blocks=n_blocks, max_blocks=width, batch=1,
+                     out_dtype=rkv.RKV_DTYPE_F32)
+    for codes, scale in ((cache.codes_K, cache.scale_K), (cache.codes_V, cache.scale_V)):
+        codes.copy_((torch.randn(codes.shape, generator=g) * 30).round().clamp(-127, 127).to(torch.int8))
+        scale.fill_(1 / 32)
+    q, out = values(g, (1, 2, d), torch.bfloat16).cuda(), torch.empty((1, 2, d), device="cuda")
+    table = torch.full((1, width), 1, dtype=torch.int32, device="cuda")
+    k, v = (c[1].double().cpu().transpose(0, 1) / 32 for c in (cache.codes_K, cache.codes_V))
+    want, _, mag, spread = ref.attention(q.cpu(), k, v, torch.ones((1, block), dtype=torch.bool))
+    tol, _ = ref.bounds(want, mag, spread, d, block, torch.float16, torch.float32, 2.0 ** -40 * 127 / 32)
+    tol = tol + mag * 2 * (56680 + 10) * 2.0 ** -24
+    cache.decode(q, table, ints([2 ** 31 - 1]), out)
+    assert cache.device_error() == rkv.STATUS_CODE["RKV_ERR_CORRUPT"]
+    assert ((out.double().cpu() - want).abs() <= tol).all()
+    cache.decode(q, table, ints([2 ** 31 - 65]), out)            # one token less in the last block
+    assert cache.device_error() == 0
+    assert ((out.double().cpu() - want).abs() <= tol).all()
+
+
 # --- prompt attention -------------------------------------------------------------------------
 
 FAR = [(torch.bfloat16, e) for e in (12, 15, 16, 17, 20, 22, 24, 26, 28, 31, 36, 60, 100)] + \

@@ -161,6 +161,17 @@ def test_kv8_refuses_configurations(call, kw, code):
     assert call(kv8_cfg(**kw)) == code
 
 
+@pytest.mark.parametrize("call", [store_status, decode_status, size_status])
+def test_kv8_refuses_rows_next_to_31_bits(call):
+    # lengths are rounded up to tiles of 64 tokens in 31 bits
+    for block, most in ((16, 2 ** 27 - 4), (32, 2 ** 26 - 2), (64, 2 ** 25 - 1), (128, 2 ** 24 - 1)):
+        for blocks in (most + 1, 2 ** 31 // block - 1):
+            if blocks > most:
+                assert call(kv8_cfg(block_size=block, max_blocks=blocks)) == UNSUPPORTED
+        largest = kv8_cfg(block_size=block, max_blocks=most, **({} if call is size_status else dict(codes_K=None)))
+        assert call(largest) == (0 if call is size_status else INVALID)      # the next check
+
+
 @pytest.mark.parametrize("call", [store_status, decode_status])
 def test_kv8_refuses_buffers(call):
     assert call(None) == INVALID
