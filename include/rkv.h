@@ -444,7 +444,7 @@ RKV_API rkv_status rkv_selftest_wait_timeout(int32_t* err_dev, void* stream);
  *                   (packed).  1: sequence b has a plane of kv_rows rows of its own, `kv_plane_stride`
  *                   apart (the layout that rkv_build_refs and rkv_compress read)
  *   scale           factor of q.k before the softmax; 0 means 1/sqrt(head_dim); otherwise > 0, at most 2^127
- *   q_rows          rows of q, out and lse;  kv_rows  rows of a plane of K and V
+ *   q_rows          rows of q, out and lse;  kv_rows  rows of a plane of K and V; each at most 2^31 - 256
  *   *_stride        element strides: of a row (token), of a head, of a plane.  Those of q, K and V are
  *                   multiples of 8 and rows of one head are head_dim contiguous elements; out_*
  *                   multiples of 8 for 16-bit outputs and of 4 for 32-bit ones.

@@ -69,7 +69,8 @@ rkv_status check_prefill(const rkv_prefill_config* c)
     if (!half_type(c->in_dtype) || (c->out_dtype != c->in_dtype && c->out_dtype != RKV_DTYPE_F32) ||
         (c->kv_padded != 0 && c->kv_padded != 1) || !scale_ok(c->scale) || c->q_rows < 0 || c->kv_rows < 0)
         return RKV_ERR_INVALID_ARG;
-    if (c->q_rows > INT32_MAX || c->kv_rows > INT32_MAX)
+    // rows are rounded up to query tiles of up to 128 tokens, two at a time, and keys to tiles of 64, in 31 bits
+    if (c->q_rows > INT32_MAX - 255 || c->kv_rows > INT32_MAX - 255)
         return RKV_ERR_UNSUPPORTED;
     const int64_t out_unit = c->out_dtype == RKV_DTYPE_F32 ? 4 : 8;
     if (!stride_ok(c->q_row_stride, 8) || !stride_ok(c->q_head_stride, 8) || !stride_ok(c->kv_row_stride, 8) ||

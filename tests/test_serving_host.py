@@ -60,6 +60,14 @@ def test_prefill_refuses_configurations(kw, code):
     assert prefill_status(prefill_cfg(**kw)) == code
 
 
+@pytest.mark.parametrize("rows", ["q_rows", "kv_rows"])
+def test_prefill_refuses_rows_next_to_31_bits(rows):
+    # tokens are rounded up to tiles in 31 bits
+    for n in (2 ** 31 - 255, 2 ** 31 - 1):
+        assert prefill_status(prefill_cfg(**{rows: n})) == UNSUPPORTED
+    assert prefill_status(prefill_cfg(**{rows: 2 ** 31 - 256}), out=None) == INVALID       # the next check
+
+
 def test_prefill_refuses_pointers():
     assert prefill_status(None) == INVALID
     cfg = prefill_cfg()
