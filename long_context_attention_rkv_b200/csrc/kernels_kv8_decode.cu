@@ -32,8 +32,10 @@
 // its largest element lies in [2^14, 2^15): every element is then exact or, if tiny, off by at most 2^-40 of
 // the largest.
 //
-// Measured: 4 requests of 131072 tokens, 32 / 8 heads of 128: 183 us = 5.85 TB/s (0.90 of the measured copy rate); 8 ragged
-// requests of 16384 to 32768, 28 / 4 heads: 47.7 us; one of 2049: 7.5 us, latency.
+// Measured: 4 requests of 131072 tokens, 32 / 8 heads of 128: 172 us in a burst = 6.25 TB/s (0.95 of the measured copy rate), 195 us
+// when thousands of calls go on and power lowers the clock; of 64 (half the bytes in flight) 120 us = 4.5 TB/s; 32 / 2 heads
+// of 128 (two CTAs per SM) 80 us = 3.3 TB/s.  8 ragged requests of 16384 to 32768, 28 / 4 heads: 47.5 us; 64 of 1024, 32 / 8
+// heads: 35.5 us; one of 2049: 7 us, latency.
 //
 // Work split: units (request, kv-head) are cut into tiles of 64 tokens; a CTA's four warps take 16 tokens of each tile, and
 // at the end of a unit their states are merged.  Short rows: a cluster per unit, whose CTAs take equal ranges of its tiles
@@ -57,7 +59,7 @@ using namespace kv8;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16 * kWarps;     // tokens per CTA step
-constexpr int kCtasPerSm = 4;          // at 128 registers; 4 requests of 131072 tokens: 183 us, three 191 us, two 246 us
+constexpr int kCtasPerSm = 4;          // at 128 registers; 4 requests of 131072 tokens: 172 us, three 186 us, two 236 us
 constexpr int kMaxCtas = 160 * kCtasPerSm;
 constexpr float kNone = -FLT_MAX;      // logit before any token
 constexpr float kZeroScale = -64.0f;   // log2 of the scale that a scale of 0 has in the maximum (kMinScale)
@@ -796,9 +798,11 @@ cudaError_t launch_d(const DecodeArgs& a, bool e4m3, bool f16, int ctas, int par
 // CTAs of a cluster per unit, 0 for the form with the workspace and the join kernel.  What the host knows are the units and
 // the tiles that a table row can hold, so a cluster is taken where its CTAs have at most 8 tiles even of a full row (one
 // long request among short ones then costs little), as many CTAs as run at once.  32 / 8 heads of 128, with join kernel
-// and in clusters of 1 / 2 / 4 / 8: 1 request of 512 tokens 6.7 and 10.5 / 7.2 / 5.5 / 5.0 us, of 2049 8.6 and 27 / 15.6 /
-// 10.1 / 7.5, of 8192 13.2 and 90 / 47 / 26 / 15.2; 8 of 2049 15.6 and 27 / 16.1 / 11.8 / 11.6; 64 of 1024 38.1 and 32.3 /
-// 35.5 / 43 / 61, of 2049 61 and 56 / 59 / 67 / 85.  It also saves the host a launch (2 us).
+// and in clusters of 1 / 2 / 4 / 8: 1 request of 512 tokens 6.4 and 9.9 / 6.8 / 5.4 / 4.8 us, of 2049 8.1 and 25 / 14.8 /
+// 9.5 / 7.3, of 8192 12.4 and 82 / 43 / 24 / 14.4; 8 of 2049 14.3 and 26 / 15.2 / 11.5 / 11.6; 64 of 1024 35.9 and 32.4 /
+// 35.6 / 44 / 62, of 2049 57 and 56 / 59 / 67 / 85.  It also saves the host a launch (2 us).  Rows that could hold much more take
+// the other form: with rows of 32768 tokens, one request of 512 6.4 us instead of 4.8, of 2049 8.7 instead of 7.0, 8 of
+// 2049 14.3 instead of 11.7.
 int cluster_parts(const rkv_kv8_cache& c, int sms)
 {
     constexpr int64_t kTiles = 8;

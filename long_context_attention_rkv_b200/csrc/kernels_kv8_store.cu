@@ -8,8 +8,12 @@
 // Growing the scale by powers of two bounds what repeated growth costs: the roundings of an old row are
 // at most s'/2 + s'/4 + ... < s', however many tokens the block receives one by one.
 //
-// 2 bytes read and 1 written per element; 32768 tokens x 8 heads x 128 take 39.8 us (4.4 TB/s), of which the conversion
-// adds 13 to the 27 that moving the bytes takes: the kernel is bound by instruction issue.  One CTA does the K or the V side of the runs
+// 2 bytes read and 1 written per element; 28616 tokens x 8 heads x 128 take 39.7 us (4.4 TB/s; both code types, values with a
+// few large channels), of which the conversion adds 13 to the 27 that moving the bytes takes: the kernel is bound by
+// instruction issue (72 to 75 % of its slots).  Either type executes 16.8 instructions per value, 46 % of them on the
+// integer pipe (67 to 69 % busy): two conversions, or two fused multiply-adds and the gathering of their low bytes, the
+// comparison of the two results, the maximum and the widening.
+// One CTA does the K or the V side of the runs
 // that start in one window of packed rows, for one head; it holds a run (at most one block of rows) in
 // registers between the maximum and the codes, so the rows are read once.  A window is about one run long (window_of
 // below): one block's worth of rows for prompts, a single row for decode steps, so that all runs go side by side.  The CTA has block * head_dim / 64 threads, so that each holds
@@ -112,7 +116,9 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint64_t v)
     return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Eight int8 codes by division; rare (1 piece in 2000 of normal values), and kept out of line.
+// Eight int8 codes by division, kept out of line: 1 piece in 1300 where a few channels are large (2 % of the warps see one).  Of
+// plain normal values 1 in 40, most of them in blocks whose largest value is 254 times a power of two (x / s is then half an odd
+// number for every odd significand): 28616 tokens x 8 heads x 128 of those take 47.8 us, in e4m3 39.5 us.
 __device__ __noinline__ uint2 divide8(float4 a, float4 b, float s)
 {
     const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -162,7 +168,7 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint64_t lo, uin
 
 // e4m3: the codes of the open bytes by division, one by one; v: the values as 16-bit words, the first in the low half of
 // v.x.  Quotients of two 8-bit significands times 448 = 7 * 64 lie on a border of 4-bit codes often (one value in a
-// few hundred, so most warps see one): dividing whole pieces costs 32768 tokens x 8 heads x 128 4 us more.
+// few hundred, so most warps see one): dividing whole pieces costs 28616 tokens x 8 heads x 128 4 us more.
 template <bool kF16>
 __device__ __forceinline__ void settle(const uint4& v, float s, uint2& o, uint2 open)
 {
@@ -389,7 +395,7 @@ cudaError_t launch_t(const StoreArgs& a, bool f16, dim3 grid, cudaStream_t st)
 // window has about one run: a CTA does several runs one after the other, and a CTA without a run costs its look at the
 // slots.  Fewer rows where that leaves less than four of these small CTAs per SM.  8 heads x 128, blocks of 64, windows
 // of 1 / 4 / 16 / 64 rows: 64 requests with 1 token each 4.6 us, in windows of 64 66 us; with 4 to 8 9.8 / 6.3 / 7.0 /
-// 16.8 us; with 12 to 24 20.6 / 9.9 / 7.0 / 9.5 us; 4 with 100 to 200 10.8 / 6.0 / 4.4 / 6.7 us; 1 with 32768 411 us in
+// 16.8 us; with 12 to 24 20.6 / 9.9 / 7.0 / 9.5 us; 4 with 100 to 200 10.8 / 6.0 / 4.4 / 6.7 us; 1 with 28616 411 us in
 // windows of 1, 39.4 us in windows of 64.
 int window_of(int64_t n_rows, const rkv_kv8_cache& c, int sms)
 {

@@ -32,10 +32,11 @@
 //
 // Warps: 0 TMA producer, 1 and 2 issue S of query tiles 0 and 1, 3 issues P V of both, 4-7 and 8-11 are their softmax.
 //
-// Measured: 8192 tokens, 32 query and 8 kv-heads of 128: 440 us = 1250 TFLOP/s (0.91 of the sustained rate of a plain
-// product; about 1530 cycles per 64 keys of two query tiles, 1280 of them products, at the 1.65 GHz that the board's
-// power allows).  8 ragged prompts of 300 to 2500 tokens 91 us, where the roughly 5000 cycles of an item outside its steps
-// (first loads and S, last product, output) count.
+// Measured: 8192 tokens, 32 query and 8 kv-heads of 128: 445 to 490 us in a burst of ten calls = 1235 to 1120 TFLOP/s, 510 us =
+// 1080 TFLOP/s (0.78 of the sustained rate of a plain product) when calls go on and the board's power holds the clock at
+// 1.58 GHz; at 1.65 GHz about 1530 cycles per 64 keys of two query tiles, 1280 of them products.  8 ragged prompts of 300
+// to 2500 tokens 90 us (burst; 104 us), where the roughly 5000 cycles of an item outside its steps (first loads and S, last product,
+// output) count.
 //
 // Every wait is bounded (2 s); one that gives up records RKV_ERR_TIMEOUT, all roles leave their loops, and copies
 // and products in flight are waited for before TMEM is freed.
